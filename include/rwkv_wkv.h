@@ -338,6 +338,175 @@ RWKV_API rwkv_status rwkv_wkv6_backward(int64_t B, int64_t T, int64_t H, int64_t
                                float *gomega, float *gu, float *gs_in, void *workspace, size_t workspace_bytes,
                                rwkv_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * The operators around the recurrence: a short causal convolution, a selective
+ * state space scan and the layer norm.  The conventions above hold (device
+ * pointers, caller-owned memory, no synchronisation, status codes, zero-sized
+ * problems are a no-op), and:
+ *   - dtype (fp32 or bf16) is the element type of the activations and their
+ *     gradients; parameters, their gradients and the scan's states are fp32.
+ *     Arithmetic and sums are fp32, each output is rounded once.
+ *   - `ld*` is the distance in elements between the rows of an input (one row
+ *     per token: element (b, t, c) of x is x[(b T + t) ldx + c]), at least the
+ *     row's length, so that a part of a wider tensor can be passed without a
+ *     copy.  Tensors without an ld are dense.
+ *   - Pointers aligned to their element size are served; where every base is
+ *     16-byte aligned and every row length and ld a multiple of 16 bytes the
+ *     accesses are wide.  The scan's states and checkpoints and every workspace must be
+ *     16-byte aligned (RWKV_ERR_UNSUPPORTED otherwise).
+ *   - Outputs must not overlap inputs or one another, except where a call says
+ *     that a state may be updated in place.
+ *   - A workspace belongs to one call until the stream has run it: calls that
+ *     may overlap (other streams, graphs replayed together) need their own.
+ *   - Deterministic: no atomics, sums in a fixed order.
+ *   - Sizes whose launches would pass 2^31 - 1 blocks give RWKV_ERR_UNSUPPORTED.
+ * ------------------------------------------------------------------------- */
+
+/* Activation behind the causal convolution: none, or silu(p) = p / (1 + e^{-p}). */
+typedef enum { RWKV_ACT_NONE = 0, RWKV_ACT_SILU = 1 } rwkv_act;
+
+/*
+ * Causal convolution over time, one filter of W taps (2, 3 or 4;
+ * RWKV_ERR_UNSUPPORTED otherwise) per channel:
+ *   y_t[c] = act(bias[c] + sum_{j<W} weight[c][j] x_{t-W+1+j}[c]).
+ * The token shift mu x_t + (1 - mu) x_{t-1} is W = 2 with weight (1 - mu, mu).
+ *   weight    [C,W] fp32.   bias [C] fp32 or NULL (zero).
+ *   x         [B,T,C] dtype, rows ldx apart.   y [B,T,C] dtype, written.
+ *   state_in  [B,W-1,C] dtype: the W-1 tokens before the first, oldest first,
+ *             or NULL (zeros).   state_out [B,W-1,C] or NULL: the last W-1
+ *             tokens (of state_in too, when T < W-1); may equal state_in.
+ */
+RWKV_API rwkv_status rwkv_causal_conv_forward(int64_t B, int64_t T, int64_t C, int64_t W, rwkv_dtype dtype,
+                                     const float *weight, const float *bias, int act, const void *x,
+                                     int64_t ldx, void *y, const void *state_in, void *state_out,
+                                     rwkv_stream_t stream);
+
+/* Workspace bytes rwkv_causal_conv_backward needs (0 for an empty problem). */
+RWKV_API size_t rwkv_causal_conv_backward_workspace_bytes(int64_t B, int64_t T, int64_t C, int64_t W);
+
+/*
+ * Backward of the causal convolution for L = sum gy y + sum gstate_out state_out;
+ * with g_t = gy_t act'(pre_t) (pre is formed again from x):
+ *   gx_t = sum_j weight[.][j] g_{t+W-1-j} (+ gstate_out's row of that token),
+ *   gweight[c][j] = sum_{b,t} g_t x_{t-W+1+j},   gbias = sum_{b,t} g_t.
+ *   gy        [B,T,C] dtype.   gstate_out [B,W-1,C] dtype or NULL (zero).
+ *   gx        [B,T,C] dtype, written.
+ *   gweight   [C,W], gbias [C] fp32, OVERWRITTEN; gbias may be NULL (not wanted).
+ *   gstate_in [B,W-1,C] dtype, written, or NULL (not wanted).
+ */
+RWKV_API rwkv_status rwkv_causal_conv_backward(int64_t B, int64_t T, int64_t C, int64_t W, rwkv_dtype dtype,
+                                      const float *weight, const float *bias, int act, const void *x,
+                                      int64_t ldx, const void *state_in, const void *gy,
+                                      const void *gstate_out, void *gx, float *gweight, float *gbias,
+                                      void *gstate_in, void *workspace, size_t workspace_bytes,
+                                      rwkv_stream_t stream);
+
+/* One token for each of B streams: rwkv_causal_conv_forward with T = 1.  x [B,C] (rows ldx apart),
+ * y [B,C], state_in [B,W-1,C] or NULL (zeros), state_out required; may equal state_in. */
+RWKV_API rwkv_status rwkv_causal_conv_step(int64_t B, int64_t C, int64_t W, rwkv_dtype dtype, const float *weight,
+                                  const float *bias, int act, const void *x, int64_t ldx, void *y,
+                                  const void *state_in, void *state_out, rwkv_stream_t stream);
+
+/* Workspace bytes rwkv_selective_scan_forward needs for this shape and algo (0 if none). */
+RWKV_API size_t rwkv_selective_scan_forward_workspace_bytes(int64_t B, int64_t T, int64_t C, int64_t N, int algo);
+
+/*
+ * Selective scan forward: a recurrence with a diagonal state of N values per
+ * channel, whose step size, input and output weights come from the tokens.
+ *   D_t = log(1 + exp(dt_t + dt_bias)),   A = -exp(a_log),
+ *   h_t[c][n] = exp(D_t[c] A[c][n]) h_{t-1}[c][n] + D_t[c] x_t[c] b_t[n],
+ *   p_t[c] = sum_n c_t[n] h_t[c][n] + d[c] x_t[c],
+ *   y_t = p_t, or with a gate z: y_t = p_t z_t / (1 + e^{-z_t}).
+ *   a_log     [C,N] fp32.   d, dt_bias [C] fp32 or NULL (zero).
+ *   x, dt     [B,T,C] dtype.   b, c [B,T,N] dtype.   z [B,T,C] dtype or NULL (no gate; ldz unused).
+ *   y         [B,T,C] dtype, written, or NULL (states only).
+ *   h_in      [B,C,N] fp32 or NULL (zero).   h_out [B,C,N] or NULL; may equal h_in.
+ *   ckpt      [ceil(T/chunk_len),B,C,N] fp32 or NULL: ckpt[j] is the state before token
+ *             j chunk_len (ckpt[0] = h_in), for the backward.  chunk_len must be 16 today.
+ *   algo      rwkv_algo: CHUNKED cuts time into segments that run in parallel (for few channels and
+ *             long sequences); needs the workspace.
+ *   N         8, 16, 32 or 64 (RWKV_ERR_UNSUPPORTED otherwise).
+ */
+RWKV_API rwkv_status rwkv_selective_scan_forward(int64_t B, int64_t T, int64_t C, int64_t N, rwkv_dtype dtype,
+                                        const float *a_log, const float *d, const float *dt_bias,
+                                        const void *x, int64_t ldx, const void *dt, int64_t lddt,
+                                        const void *b, int64_t ldb, const void *c, int64_t ldc,
+                                        const void *z, int64_t ldz, void *y, const float *h_in,
+                                        float *h_out, float *ckpt, int64_t chunk_len, int algo,
+                                        void *workspace, size_t workspace_bytes, rwkv_stream_t stream);
+
+/* Workspace bytes rwkv_selective_scan_backward needs (0 for an empty problem); have_ckpt = 0 adds
+ * room to form the checkpoints again. */
+RWKV_API size_t rwkv_selective_scan_backward_workspace_bytes(int64_t B, int64_t T, int64_t C, int64_t N,
+                                                    int64_t chunk_len, int have_ckpt);
+
+/*
+ * Backward of the selective scan for L = sum gy y + sum gh_out h_out.  With g_t = gy_t silu(z_t)
+ * (gy_t without a gate), e_t = exp(D_t A), G_t = c_t g_t + e_{t+1} G_{t+1} (gh_out behind the end):
+ *   gc_t[n] = sum_c g_t h_t[.][n],   gb_t[n] = sum_c G_t[.][n] D_t x_t,
+ *   s1 = sum_n G_t b_t,   q_t = G_t e_t h_{t-1},
+ *   gx_t = D_t s1 + d g_t,   gdt_t = (x_t s1 + sum_n q_t A) / (1 + e^{-(dt_t + dt_bias)}),
+ *   gdt_bias = sum_{b,t} gdt_t,   ga_log = A sum_{b,t} q_t D_t,   gd = sum_{b,t} g_t x_t,
+ *   gz_t = gy_t p_t silu'(z_t),   gh_in = e_0 G_0.
+ *   gy        [B,T,C] dtype.   h_in the forward's (used only when ckpt is NULL).
+ *   gh_out    [B,C,N] fp32 or NULL (zero).
+ *   ckpt      the forward's checkpoints (same inputs, chunk_len 16), or NULL to form them again in
+ *             the workspace.
+ *   gx, gdt   [B,T,C] dtype, gb, gc [B,T,N] dtype, written.   gz [B,T,C] dtype, required with z.
+ *   ga_log    [C,N], gd, gdt_bias [C] fp32, OVERWRITTEN; gd and gdt_bias may be NULL (not wanted).
+ *   gh_in     [B,C,N] fp32 or NULL (not wanted); may equal gh_out.
+ */
+RWKV_API rwkv_status rwkv_selective_scan_backward(int64_t B, int64_t T, int64_t C, int64_t N, rwkv_dtype dtype,
+                                         const float *a_log, const float *d, const float *dt_bias,
+                                         const void *x, int64_t ldx, const void *dt, int64_t lddt,
+                                         const void *b, int64_t ldb, const void *c, int64_t ldc,
+                                         const void *z, int64_t ldz, const void *gy, const float *h_in,
+                                         const float *gh_out, const float *ckpt, int64_t chunk_len, void *gx,
+                                         void *gdt, void *gb, void *gc, void *gz, float *ga_log, float *gd,
+                                         float *gdt_bias, float *gh_in, void *workspace,
+                                         size_t workspace_bytes, rwkv_stream_t stream);
+
+/* One token for each of B streams: rwkv_selective_scan_forward with T = 1.  x, dt, z [B,C] and
+ * b, c [B,N] (rows ld* apart), y [B,C]; h_in [B,C,N] or NULL (zero), h_out required; may equal
+ * h_in. */
+RWKV_API rwkv_status rwkv_selective_scan_step(int64_t B, int64_t C, int64_t N, rwkv_dtype dtype, const float *a_log,
+                                     const float *d, const float *dt_bias, const void *x, int64_t ldx,
+                                     const void *dt, int64_t lddt, const void *b, int64_t ldb,
+                                     const void *c, int64_t ldc, const void *z, int64_t ldz, void *y,
+                                     const float *h_in, float *h_out, rwkv_stream_t stream);
+
+/*
+ * Layer norm over the N columns of each of G groups of M rows, with an optional gate:
+ *   xh = (x - mean x) / sqrt(var x + eps),   l = xh weight + bias,
+ *   y = l, or with a gate: y = l gate / (1 + e^{-gate}).
+ * var is the mean of (x - mean)^2.  G = 1 is the norm in front of a block's mixers; G = H, N = 64
+ * with a gate is the head-wise norm and SiLU gate behind the Eagle and Finch operators, on their
+ * y [B,T,H,N] with M = B T.
+ *   x, gate, y   [M,G,N] dtype; gate may be NULL; y may equal neither.
+ *   weight, bias [G,N] fp32; bias may be NULL (zero).
+ *   eps          >= 0 and finite (RWKV_ERR_INVALID_ARG otherwise); G N at most 2^30 - 1.
+ */
+RWKV_API rwkv_status rwkv_layer_norm_forward(int64_t M, int64_t G, int64_t N, rwkv_dtype dtype, const float *weight,
+                                    const float *bias, float eps, const void *x, const void *gate,
+                                    void *y, rwkv_stream_t stream);
+
+/* Workspace bytes rwkv_layer_norm_backward needs (0 for an empty problem). */
+RWKV_API size_t rwkv_layer_norm_backward_workspace_bytes(int64_t M, int64_t G, int64_t N, rwkv_dtype dtype);
+
+/*
+ * Backward of the layer norm for L = sum gy y.  With g = gy silu(gate) (gy without a gate) and
+ * u = g weight, per row and group:
+ *   gx = (u - mean u - xh mean(u xh)) / sqrt(var x + eps),
+ *   gweight = sum_rows g xh,   gbias = sum_rows g,   ggate = gy l silu'(gate).
+ *   gx, ggate    [M,G,N] dtype, written; ggate required with gate.
+ *   gweight, gbias [G,N] fp32, OVERWRITTEN; gbias may be NULL (not wanted).
+ */
+RWKV_API rwkv_status rwkv_layer_norm_backward(int64_t M, int64_t G, int64_t N, rwkv_dtype dtype, const float *weight,
+                                     const float *bias, float eps, const void *x, const void *gate,
+                                     const void *gy, void *gx, void *ggate, float *gweight,
+                                     float *gbias, void *workspace, size_t workspace_bytes,
+                                     rwkv_stream_t stream);
+
 /* Largest B * C that rwkv_wkv4_backward_noalloc accepts. */
 #define RWKV_NOALLOC_MAX_LANES 262144
 

@@ -23,7 +23,9 @@ __all__ = [
     "ALGO_CHUNKED", "CHUNK_LEN", "NOALLOC_MAX_LANES", "rwkv_wkv4_forward", "rwkv_wkv4_backward",
     "rwkv_wkv4_backward_noalloc", "rwkv_wkv4_step", "rwkv_wkv4_forward_gated", "rwkv_wkv4_backward_gated",
     "rwkv_wkv5_forward", "rwkv_wkv5_backward", "rwkv_wkv5_step", "rwkv_wkv6_forward", "rwkv_wkv6_backward",
-    "rwkv_wkv6_step", "rwkv_check_device_error",
+    "rwkv_wkv6_step", "rwkv_causal_conv_forward", "rwkv_causal_conv_backward", "rwkv_causal_conv_step",
+    "rwkv_selective_scan_forward", "rwkv_selective_scan_backward", "rwkv_selective_scan_step",
+    "rwkv_layer_norm_forward", "rwkv_layer_norm_backward", "rwkv_check_device_error",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "librwkv_wkv.so")
@@ -76,6 +78,19 @@ def lib():
         "rwkv_wkv6_backward_workspace_bytes": ([I64, I64, I64, I64], S),
         "rwkv_wkv6_backward": ([I64, I64, I64, I64] + [P] * 15 + [S, P], I),
         "rwkv_wkv6_step": ([I64, I64, I64, P, P, P, P, P, P, P, P, P], I),
+        "rwkv_causal_conv_forward": ([I64] * 4 + [I, P, P, I, P, I64, P, P, P, P], I),
+        "rwkv_causal_conv_backward_workspace_bytes": ([I64] * 4, S),
+        "rwkv_causal_conv_backward": ([I64] * 4 + [I, P, P, I, P, I64] + [P] * 8 + [S, P], I),
+        "rwkv_causal_conv_step": ([I64] * 3 + [I, P, P, I, P, I64, P, P, P, P], I),
+        "rwkv_selective_scan_forward_workspace_bytes": ([I64] * 4 + [I], S),
+        "rwkv_selective_scan_forward": ([I64] * 4 + [I, P, P, P] + [P, I64] * 5 + [P, P, P, P, I64, I, P, S, P], I),
+        "rwkv_selective_scan_backward_workspace_bytes": ([I64] * 5 + [I], S),
+        "rwkv_selective_scan_backward": ([I64] * 4 + [I, P, P, P] + [P, I64] * 5 + [P] * 4 + [I64] + [P] * 10
+                                         + [S, P], I),
+        "rwkv_selective_scan_step": ([I64] * 3 + [I, P, P, P] + [P, I64] * 5 + [P] * 4, I),
+        "rwkv_layer_norm_forward": ([I64] * 3 + [I, P, P, ctypes.c_float] + [P] * 4, I),
+        "rwkv_layer_norm_backward_workspace_bytes": ([I64] * 3 + [I], S),
+        "rwkv_layer_norm_backward": ([I64] * 3 + [I, P, P, ctypes.c_float] + [P] * 8 + [S, P], I),
         "rwkv_check_device_error": ([P], I),
         "rwkv_debug_set_wait_limit_ns": ([ctypes.c_uint64], I),
         "rwkv_debug_withhold_loads": ([I], I),
@@ -463,6 +478,366 @@ def rwkv_wkv6_step(r, k, v, omega, u, state=None, *, state_out=None, stream=None
            lib().rwkv_wkv6_step(B, H, N, _ptr(r), _ptr(k), _ptr(v), _ptr(omega), _ptr(u), _ptr(y), _ptr(state),
                                 _ptr(so), _stream(stream)))
     return y, so
+
+
+# ------------------------------------------------------------------ around the recurrence
+def _io_code(name, t):
+    import torch
+
+    if t.dtype == torch.float32:
+        return F32
+    if t.dtype == torch.bfloat16:
+        return BF16
+    raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+
+
+def _need_here(stream, **tensors):
+    """Every tensor (and the stream) on the current CUDA device, where the call launches."""
+    import torch
+
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor (use .cuda())")
+        if t.device.index != torch.cuda.current_device():
+            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    if stream is not None and stream.device.index != torch.cuda.current_device():
+        raise ValueError(f"stream is on {stream.device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _dense(name, t, shape, dtype):
+    if t is None:
+        return
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _rows(name, t, shape, dtype):
+    """Elements between the rows of t, whose last dimension is dense and whose rows lie at equal
+    distances (a whole tensor, or a part of a wider one's last dimension)."""
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    width = t.shape[-1]
+    if t.numel() == 0:
+        return width
+    if width > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: the last dimension must be dense")
+    ld, inner = None, 1
+    for size, st in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if size == 1:
+            continue
+        if ld is None:
+            ld = st
+        elif st != ld * inner:
+            raise ValueError(f"{name}: rows must lie at equal distances, got strides {t.stride()}")
+        inner *= size
+    ld = width if ld is None else ld
+    if ld < width:
+        raise ValueError(f"{name}: rows overlap, got strides {t.stride()}")
+    return ld
+
+
+class _Launch:
+    """Allocations of one call belong to the stream it launches on; when that is not the current
+    stream, the tensors it shares with the current one are recorded on both."""
+
+    def __init__(self, stream):
+        import torch
+
+        self.current = torch.cuda.current_stream()
+        self.stream = self.current if stream is None else stream
+        self.other = self.stream.cuda_stream != self.current.cuda_stream
+        self.outputs = []
+
+    def _empty(self, shape, dtype, device):
+        import torch
+
+        if not self.other:
+            return torch.empty(shape, dtype=dtype, device=device)
+        with torch.cuda.stream(self.stream):
+            return torch.empty(shape, dtype=dtype, device=device)
+
+    def out(self, like, shape, dtype):
+        t = self._empty(shape, dtype, like.device)
+        self.outputs.append(t)
+        return t
+
+    def workspace(self, like, nbytes):
+        import torch
+
+        return self._empty((nbytes,), torch.uint8, like.device) if nbytes else None
+
+    def ptr(self):
+        return ctypes.c_void_p(self.stream.cuda_stream)
+
+    def done(self, *given):
+        if self.other:
+            for t in self.outputs:
+                t.record_stream(self.current)
+            for t in given:
+                if t is not None:
+                    t.record_stream(self.stream)
+
+
+ACT_NONE, ACT_SILU = 0, 1
+
+
+def rwkv_causal_conv_forward(x, weight, bias=None, state_in=None, *, silu=False, return_state=False, stream=None,
+                             out=None):
+    """Causal convolution over time, one filter of W = 2, 3 or 4 taps per channel:
+    y_t = act(bias + sum_j weight[:, j] x_{t-W+1+j}), act the identity or (``silu``) silu.
+
+    x [B,T,C] (fp32 or bf16; rows may be part of a wider tensor); weight [C,W], bias [C] fp32;
+    state_in [B,W-1,C] like x, the tokens before the first, or None (zeros).  Returns y, plus the
+    last W-1 tokens [B,W-1,C] if ``return_state``."""
+    import torch
+
+    _need_here(stream, x=x, weight=weight, bias=bias, state_in=state_in, out=out)
+    code = _io_code("x", x)
+    B, T, C = x.shape
+    W = weight.shape[-1]
+    _dense("weight", weight, (C, W), torch.float32)
+    _dense("bias", bias, (C,), torch.float32)
+    _dense("state_in", state_in, (B, W - 1, C), x.dtype)
+    _dense("out", out, (B, T, C), x.dtype)
+    ldx = _rows("x", x, (B, T, C), x.dtype)
+    L = _Launch(stream)
+    y = L.out(x, (B, T, C), x.dtype) if out is None else out
+    st = L.out(x, (B, W - 1, C), x.dtype) if return_state else None
+    _check("rwkv_causal_conv_forward",
+           lib().rwkv_causal_conv_forward(B, T, C, W, code, _ptr(weight), _ptr(bias), ACT_SILU if silu else ACT_NONE,
+                                          _ptr(x), ldx, _ptr(y), _ptr(state_in), _ptr(st), L.ptr()))
+    L.done(x, weight, bias, state_in, out)
+    return (y, st) if return_state else y
+
+
+def rwkv_causal_conv_backward(x, weight, gy, bias=None, state_in=None, gstate_out=None, *, silu=False,
+                              want_gstate_in=False, stream=None):
+    """Gradients of sum(gy * y) + sum(gstate_out * state_out) of ``rwkv_causal_conv_forward``:
+    returns (gx, gweight, gbias) and, with ``want_gstate_in``, the gradient of state_in as well;
+    gbias is None where bias is."""
+    import torch
+
+    _need_here(stream, x=x, weight=weight, gy=gy, bias=bias, state_in=state_in, gstate_out=gstate_out)
+    code = _io_code("x", x)
+    B, T, C = x.shape
+    W = weight.shape[-1]
+    _dense("weight", weight, (C, W), torch.float32)
+    _dense("bias", bias, (C,), torch.float32)
+    _dense("gy", gy, (B, T, C), x.dtype)
+    _dense("state_in", state_in, (B, W - 1, C), x.dtype)
+    _dense("gstate_out", gstate_out, (B, W - 1, C), x.dtype)
+    ldx = _rows("x", x, (B, T, C), x.dtype)
+    h, L = lib(), _Launch(stream)
+    gx = L.out(x, (B, T, C), x.dtype)
+    gw = L.out(x, (C, W), torch.float32)
+    gb = L.out(x, (C,), torch.float32) if bias is not None else None
+    gs = L.out(x, (B, W - 1, C), x.dtype) if want_gstate_in else None
+    wsb = int(h.rwkv_causal_conv_backward_workspace_bytes(B, T, C, W))
+    ws = L.workspace(x, wsb)
+    _check("rwkv_causal_conv_backward",
+           h.rwkv_causal_conv_backward(B, T, C, W, code, _ptr(weight), _ptr(bias), ACT_SILU if silu else ACT_NONE,
+                                       _ptr(x), ldx, _ptr(state_in), _ptr(gy), _ptr(gstate_out), _ptr(gx), _ptr(gw),
+                                       _ptr(gb), _ptr(gs), _ptr(ws), wsb, L.ptr()))
+    L.done(x, weight, gy, bias, state_in, gstate_out)
+    return (gx, gw, gb, gs) if want_gstate_in else (gx, gw, gb)
+
+
+def rwkv_causal_conv_step(x, weight, state, bias=None, *, silu=False, state_out=None, stream=None, out=None):
+    """One token for each of B streams: x [B,C]; state [B,W-1,C] like x, updated in place unless
+    ``state_out`` is given.  Returns y [B,C]."""
+    import torch
+
+    _need_here(stream, x=x, weight=weight, state=state, bias=bias, state_out=state_out, out=out)
+    code = _io_code("x", x)
+    B, C = x.shape
+    W = weight.shape[-1]
+    _dense("weight", weight, (C, W), torch.float32)
+    _dense("bias", bias, (C,), torch.float32)
+    _dense("state", state, (B, W - 1, C), x.dtype)
+    _dense("state_out", state_out, (B, W - 1, C), x.dtype)
+    _dense("out", out, (B, C), x.dtype)
+    ldx = _rows("x", x, (B, C), x.dtype)
+    L = _Launch(stream)
+    y = L.out(x, (B, C), x.dtype) if out is None else out
+    so = state if state_out is None else state_out
+    _check("rwkv_causal_conv_step",
+           lib().rwkv_causal_conv_step(B, C, W, code, _ptr(weight), _ptr(bias), ACT_SILU if silu else ACT_NONE,
+                                       _ptr(x), ldx, _ptr(y), _ptr(state), _ptr(so), L.ptr()))
+    L.done(x, weight, state, bias, state_out, out)
+    return y
+
+
+def _scan_args(x, dt, b, c, a_log, d, dt_bias, z):
+    """Checks what the scan's calls share; returns (N, the ld of x, dt, b, c and z)."""
+    import torch
+
+    lead, C, N = tuple(x.shape[:-1]), x.shape[-1], a_log.shape[-1]
+    _dense("a_log", a_log, (C, N), torch.float32)
+    _dense("d", d, (C,), torch.float32)
+    _dense("dt_bias", dt_bias, (C,), torch.float32)
+    lds = [_rows("x", x, lead + (C,), x.dtype), _rows("dt", dt, lead + (C,), x.dtype),
+           _rows("b", b, lead + (N,), x.dtype), _rows("c", c, lead + (N,), x.dtype),
+           _rows("z", z, lead + (C,), x.dtype) if z is not None else C]
+    return N, lds
+
+
+def rwkv_selective_scan_forward(x, dt, b, c, a_log, d=None, dt_bias=None, z=None, h_in=None, *, return_state=False,
+                                checkpoints=False, algo=ALGO_AUTO, stream=None, out=None):
+    """Selective scan: with D = softplus(dt + dt_bias) and A = -exp(a_log), per channel
+    h_t = exp(D_t A) h_{t-1} + D_t x_t b_t,  y_t = c_t . h_t + d x_t, times silu(z_t) if z is given.
+
+    x, dt, z [B,T,C] and b, c [B,T,N] (fp32 or bf16, all alike; rows may be parts of wider tensors);
+    a_log [C,N], d, dt_bias [C] fp32; h_in [B,C,N] fp32 or None (zero); N 8, 16, 32 or 64.  Returns
+    y, plus the final state [B,C,N] if ``return_state`` and the checkpoints [ceil(T/16),B,C,N] for
+    ``rwkv_selective_scan_backward`` if ``checkpoints``."""
+    import torch
+
+    _need_here(stream, x=x, dt=dt, b=b, c=c, a_log=a_log, d=d, dt_bias=dt_bias, z=z, h_in=h_in, out=out)
+    code = _io_code("x", x)
+    B, T, C = x.shape
+    N, (ldx, lddt, ldb, ldc, ldz) = _scan_args(x, dt, b, c, a_log, d, dt_bias, z)
+    _dense("h_in", h_in, (B, C, N), torch.float32)
+    _dense("out", out, (B, T, C), x.dtype)
+    h, L = lib(), _Launch(stream)
+    y = L.out(x, (B, T, C), x.dtype) if out is None else out
+    ho = L.out(x, (B, C, N), torch.float32) if return_state else None
+    ck = L.out(x, ((T + CHUNK_LEN - 1) // CHUNK_LEN, B, C, N), torch.float32) if checkpoints else None
+    wsb = int(h.rwkv_selective_scan_forward_workspace_bytes(B, T, C, N, algo))
+    ws = L.workspace(x, wsb)
+    _check("rwkv_selective_scan_forward",
+           h.rwkv_selective_scan_forward(B, T, C, N, code, _ptr(a_log), _ptr(d), _ptr(dt_bias), _ptr(x), ldx,
+                                         _ptr(dt), lddt, _ptr(b), ldb, _ptr(c), ldc, _ptr(z), ldz, _ptr(y),
+                                         _ptr(h_in), _ptr(ho), _ptr(ck), CHUNK_LEN, algo, _ptr(ws), wsb, L.ptr()))
+    L.done(x, dt, b, c, a_log, d, dt_bias, z, h_in, out)
+    res = (y,)
+    if return_state:
+        res += (ho,)
+    if checkpoints:
+        res += (ck,)
+    return res[0] if len(res) == 1 else res
+
+
+def rwkv_selective_scan_backward(x, dt, b, c, a_log, gy, d=None, dt_bias=None, z=None, ckpt=None, h_in=None,
+                                 gh_out=None, *, want_gh_in=False, stream=None):
+    """Gradients of sum(gy * y) + sum(gh_out * h_out) of ``rwkv_selective_scan_forward``: returns
+    (gx, gdt, gb, gc, ga_log, gd, gdt_bias, gz) and, with ``want_gh_in``, the gradient of h_in as
+    well; gd, gdt_bias and gz are None where d, dt_bias and z are.  ``ckpt`` are the forward's
+    checkpoints, or None to form them again (from ``h_in``)."""
+    import torch
+
+    _need_here(stream, x=x, dt=dt, b=b, c=c, a_log=a_log, gy=gy, d=d, dt_bias=dt_bias, z=z, ckpt=ckpt, h_in=h_in,
+               gh_out=gh_out)
+    code = _io_code("x", x)
+    B, T, C = x.shape
+    N, (ldx, lddt, ldb, ldc, ldz) = _scan_args(x, dt, b, c, a_log, d, dt_bias, z)
+    _dense("gy", gy, (B, T, C), x.dtype)
+    _dense("ckpt", ckpt, ((T + CHUNK_LEN - 1) // CHUNK_LEN, B, C, N), torch.float32)
+    _dense("h_in", h_in, (B, C, N), torch.float32)
+    _dense("gh_out", gh_out, (B, C, N), torch.float32)
+    h, L = lib(), _Launch(stream)
+    gx, gdt = L.out(x, (B, T, C), x.dtype), L.out(x, (B, T, C), x.dtype)
+    gb, gc = L.out(x, (B, T, N), x.dtype), L.out(x, (B, T, N), x.dtype)
+    gz = L.out(x, (B, T, C), x.dtype) if z is not None else None
+    ga = L.out(x, (C, N), torch.float32)
+    gd = L.out(x, (C,), torch.float32) if d is not None else None
+    gbias = L.out(x, (C,), torch.float32) if dt_bias is not None else None
+    ghi = L.out(x, (B, C, N), torch.float32) if want_gh_in else None
+    wsb = int(h.rwkv_selective_scan_backward_workspace_bytes(B, T, C, N, CHUNK_LEN, 1 if ckpt is not None else 0))
+    ws = L.workspace(x, wsb)
+    _check("rwkv_selective_scan_backward",
+           h.rwkv_selective_scan_backward(B, T, C, N, code, _ptr(a_log), _ptr(d), _ptr(dt_bias), _ptr(x), ldx,
+                                          _ptr(dt), lddt, _ptr(b), ldb, _ptr(c), ldc, _ptr(z), ldz, _ptr(gy),
+                                          _ptr(h_in), _ptr(gh_out), _ptr(ckpt), CHUNK_LEN, _ptr(gx), _ptr(gdt),
+                                          _ptr(gb), _ptr(gc), _ptr(gz), _ptr(ga), _ptr(gd), _ptr(gbias), _ptr(ghi),
+                                          _ptr(ws), wsb, L.ptr()))
+    L.done(x, dt, b, c, a_log, gy, d, dt_bias, z, ckpt, h_in, gh_out)
+    res = (gx, gdt, gb, gc, ga, gd, gbias, gz)
+    return res + (ghi,) if want_gh_in else res
+
+
+def rwkv_selective_scan_step(x, dt, b, c, a_log, state, d=None, dt_bias=None, z=None, *, state_out=None, stream=None,
+                             out=None):
+    """One token for each of B streams: x, dt, z [B,C]; b, c [B,N]; state [B,C,N] fp32, updated in
+    place unless ``state_out`` is given.  Returns y [B,C]."""
+    import torch
+
+    _need_here(stream, x=x, dt=dt, b=b, c=c, a_log=a_log, state=state, d=d, dt_bias=dt_bias, z=z,
+               state_out=state_out, out=out)
+    code = _io_code("x", x)
+    B, C = x.shape
+    N, (ldx, lddt, ldb, ldc, ldz) = _scan_args(x, dt, b, c, a_log, d, dt_bias, z)
+    _dense("state", state, (B, C, N), torch.float32)
+    _dense("state_out", state_out, (B, C, N), torch.float32)
+    _dense("out", out, (B, C), x.dtype)
+    L = _Launch(stream)
+    y = L.out(x, (B, C), x.dtype) if out is None else out
+    so = state if state_out is None else state_out
+    _check("rwkv_selective_scan_step",
+           lib().rwkv_selective_scan_step(B, C, N, code, _ptr(a_log), _ptr(d), _ptr(dt_bias), _ptr(x), ldx, _ptr(dt),
+                                          lddt, _ptr(b), ldb, _ptr(c), ldc, _ptr(z), ldz, _ptr(y), _ptr(state),
+                                          _ptr(so), L.ptr()))
+    L.done(x, dt, b, c, a_log, state, d, dt_bias, z, state_out, out)
+    return y
+
+
+def _norm_args(x, weight, bias, gate, groups):
+    """Checks what the norm's calls share; returns (M, N) for `groups` groups in x's last dimension."""
+    import torch
+
+    C = x.shape[-1]
+    if groups < 1 or C % groups != 0:
+        raise ValueError(f"groups must divide the last dimension {C}, got {groups}")
+    _dense("x", x, x.shape, x.dtype)
+    _dense("weight", weight, (C,), torch.float32)
+    _dense("bias", bias, (C,), torch.float32)
+    _dense("gate", gate, x.shape, x.dtype)
+    return (x.numel() // C if C else 0), C // groups
+
+
+def rwkv_layer_norm_forward(x, weight, bias=None, gate=None, *, groups=1, eps=1e-5, stream=None, out=None):
+    """Layer norm over each of ``groups`` equal parts of x's last dimension [..., C]:
+    (x - mean) / sqrt(var + eps) * weight + bias, times silu(gate) if a gate (like x) is given.
+    x fp32 or bf16; weight, bias [C] fp32.  groups = H on an Eagle or Finch output [B,T,H*64] is
+    the head-wise norm."""
+    _need_here(stream, x=x, weight=weight, bias=bias, gate=gate, out=out)
+    code = _io_code("x", x)
+    M, N = _norm_args(x, weight, bias, gate, groups)
+    _dense("out", out, x.shape, x.dtype)
+    L = _Launch(stream)
+    y = L.out(x, x.shape, x.dtype) if out is None else out
+    _check("rwkv_layer_norm_forward",
+           lib().rwkv_layer_norm_forward(M, groups, N, code, _ptr(weight), _ptr(bias), eps, _ptr(x), _ptr(gate),
+                                         _ptr(y), L.ptr()))
+    L.done(x, weight, bias, gate, out)
+    return y
+
+
+def rwkv_layer_norm_backward(x, weight, gy, bias=None, gate=None, *, groups=1, eps=1e-5, stream=None):
+    """Gradients of sum(gy * y) of ``rwkv_layer_norm_forward``: returns (gx, gweight, gbias, ggate);
+    gbias and ggate are None where bias and gate are."""
+    import torch
+
+    _need_here(stream, x=x, weight=weight, gy=gy, bias=bias, gate=gate)
+    code = _io_code("x", x)
+    M, N = _norm_args(x, weight, bias, gate, groups)
+    _dense("gy", gy, x.shape, x.dtype)
+    C = x.shape[-1]
+    h, L = lib(), _Launch(stream)
+    gx = L.out(x, x.shape, x.dtype)
+    gw = L.out(x, (C,), torch.float32)
+    gb = L.out(x, (C,), torch.float32) if bias is not None else None
+    gg = L.out(x, x.shape, x.dtype) if gate is not None else None
+    wsb = int(h.rwkv_layer_norm_backward_workspace_bytes(M, groups, N, code))
+    ws = L.workspace(x, wsb)
+    _check("rwkv_layer_norm_backward",
+           h.rwkv_layer_norm_backward(M, groups, N, code, _ptr(weight), _ptr(bias), eps, _ptr(x), _ptr(gate),
+                                      _ptr(gy), _ptr(gx), _ptr(gg), _ptr(gw), _ptr(gb), _ptr(ws), wsb, L.ptr()))
+    L.done(x, weight, gy, bias, gate)
+    return gx, gw, gb, gg
 
 
 def rwkv_check_device_error(stream=None):

@@ -18,7 +18,8 @@ LIB = os.path.join(PKG, "librwkv_wkv.so")
 HEADER = os.path.join(ROOT, "include", "rwkv_wkv.h")
 
 SOURCES = ["api.cu", "wkv4_fwd.cu", "wkv4_bwd.cu", "wkv4_bwd_noalloc.cu", "wkv4_step.cu", "wkv5_fwd.cu", "wkv6_fwd.cu",
-           "wkv5_step.cu", "wkv5_bwd.cu", "wkv6_bwd.cu"]
+           "wkv5_step.cu", "wkv5_bwd.cu", "wkv6_bwd.cu", "api_mixer.cu", "conv.cu", "scan_fwd.cu", "scan_bwd.cu",
+           "scan_step.cu", "norm.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

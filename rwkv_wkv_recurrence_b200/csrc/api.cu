@@ -317,7 +317,7 @@ const char* rwkv_status_string(rwkv_status s) {
   return "unknown status";
 }
 
-int rwkv_version(void) { return (1 << 16) | 2; }
+int rwkv_version(void) { return (1 << 16) | 3; }
 
 int64_t rwkv_wkv4_num_checkpoints(int64_t T, int64_t chunk_len) {
   if (chunk_len <= 0 || chunk_len % 16 != 0 || T < 0) return -1;

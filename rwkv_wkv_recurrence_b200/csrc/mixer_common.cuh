@@ -1,0 +1,109 @@
+// Device helpers shared by the operators around the WKV recurrence: the causal convolution, the
+// selective scan and the layer norm.
+#pragma once
+
+#include "wkv_common.cuh"
+
+namespace rwkv {
+
+// V consecutive elements as floats; one access where V elements are 4, 8 or 16 bytes (the caller
+// then guarantees that alignment), element by element otherwise.
+template <typename T, int V>
+__device__ __forceinline__ void load_vec(const T* p, float (&f)[V]) {
+  if constexpr (sizeof(T) == 4 && V % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+      const float4 x = *reinterpret_cast<const float4*>(p + i);
+      f[i] = x.x, f[i + 1] = x.y, f[i + 2] = x.z, f[i + 3] = x.w;
+    }
+  } else if constexpr (sizeof(T) == 4 && V == 2) {
+    const float2 x = *reinterpret_cast<const float2*>(p);
+    f[0] = x.x, f[1] = x.y;
+  } else if constexpr (sizeof(T) == 2 && V % 2 == 0) {
+    constexpr int W = V / 2;  // 32-bit words
+    uint32_t w[W];
+    if constexpr (W % 4 == 0) {
+#pragma unroll
+      for (int i = 0; i < W; i += 4) {
+        const uint4 x = *reinterpret_cast<const uint4*>(p + 2 * i);
+        w[i] = x.x, w[i + 1] = x.y, w[i + 2] = x.z, w[i + 3] = x.w;
+      }
+    } else if constexpr (W == 2) {
+      const uint2 x = *reinterpret_cast<const uint2*>(p);
+      w[0] = x.x, w[1] = x.y;
+    } else {
+      static_assert(W == 1, "16, 8 or 4 bytes");
+      w[0] = *reinterpret_cast<const uint32_t*>(p);
+    }
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  } else {
+    static_assert(V == 1, "vector width");
+    f[0] = IO<T>::to_f(*p);
+  }
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// The inverse of load_vec: rounds to nearest once.
+template <typename T, int V>
+__device__ __forceinline__ void store_vec(T* p, const float (&f)[V]) {
+  if constexpr (sizeof(T) == 4 && V % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < V; i += 4)
+      *reinterpret_cast<float4*>(p + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
+  } else if constexpr (sizeof(T) == 4 && V == 2) {
+    *reinterpret_cast<float2*>(p) = make_float2(f[0], f[1]);
+  } else if constexpr (sizeof(T) == 2 && V % 8 == 0) {
+#pragma unroll
+    for (int i = 0; i < V; i += 8)
+      *reinterpret_cast<uint4*>(p + i) = make_uint4(pack_bf16(f[i], f[i + 1]), pack_bf16(f[i + 2], f[i + 3]),
+                                                    pack_bf16(f[i + 4], f[i + 5]), pack_bf16(f[i + 6], f[i + 7]));
+  } else if constexpr (sizeof(T) == 2 && V == 4) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]));
+  } else if constexpr (sizeof(T) == 2 && V == 2) {
+    *reinterpret_cast<uint32_t*>(p) = pack_bf16(f[0], f[1]);
+  } else {
+    static_assert(V == 1, "vector width");
+    *p = IO<T>::from_f(f[0]);
+  }
+}
+
+// The first n of V elements (the rest read as zero); one wide access when `vec` and all are there.
+template <typename T, int V>
+__device__ __forceinline__ void load_part(const T* p, int n, bool vec, float (&f)[V]) {
+  if (vec && n >= V) {
+    load_vec<T, V>(p, f);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) f[i] = i < n ? IO<T>::to_f(p[i]) : 0.f;
+  }
+}
+template <typename T, int V>
+__device__ __forceinline__ void store_part(T* p, int n, bool vec, const float (&f)[V]) {
+  if (vec && n >= V) {
+    store_vec<T, V>(p, f);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (i < n) p[i] = IO<T>::from_f(f[i]);
+  }
+}
+
+// softplus(v) = log(1 + e^v) = max(v, 0) + log1p(e^-|v|) and its derivative, the logistic sigmoid;
+// both keep their relative accuracy for very negative v, where the step sizes of a scan lie.
+__device__ __forceinline__ float softplus(float v, float& sig) {
+  const float e = expf(-fabsf(v));
+  const float r = 1.f / (1.f + e);
+  sig = v >= 0.f ? r : e * r;
+  if (v != v) sig = v;
+  return fmaxf(v, 0.f) + log1pf(e) + (v != v ? v : 0.f);
+}
+
+}  // namespace rwkv
