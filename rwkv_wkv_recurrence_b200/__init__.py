@@ -481,6 +481,23 @@ def rwkv_wkv6_step(r, k, v, omega, u, state=None, *, state_out=None, stream=None
 
 
 # ------------------------------------------------------------------ around the recurrence
+# Decode calls these once per token and operator, so the checks below look at each tensor once and
+# pass plain integers on: a call costs the host little more than its launch.
+ACT_NONE, ACT_SILU = 0, 1
+_fns = {}
+
+
+def _fn(name):
+    f = _fns.get(name)
+    if f is None:
+        f = _fns[name] = getattr(lib(), name)
+    return f
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
 def _io_code(name, t):
     import torch
 
@@ -491,98 +508,102 @@ def _io_code(name, t):
     raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
 
 
-def _need_here(stream, **tensors):
-    """Every tensor (and the stream) on the current CUDA device, where the call launches."""
-    import torch
-
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor (use .cuda())")
-        if t.device.index != torch.cuda.current_device():
-            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
-    if stream is not None and stream.device.index != torch.cuda.current_device():
-        raise ValueError(f"stream is on {stream.device}, the current device is cuda:{torch.cuda.current_device()}")
-
-
-def _dense(name, t, shape, dtype):
+def _dense(name, t, shape, dtype, device):
+    """t (or None) is a contiguous tensor of this shape, type and device."""
     if t is None:
         return
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+    if t.dtype != dtype or t.shape != shape:
         raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
 
 
-def _rows(name, t, shape, dtype):
+def _rows(name, t, shape, dtype, device):
     """Elements between the rows of t, whose last dimension is dense and whose rows lie at equal
     distances (a whole tensor, or a part of a wider one's last dimension)."""
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+    if t.dtype != dtype or t.shape != shape:
         raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
-    width = t.shape[-1]
-    if t.numel() == 0:
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    width = shape[-1]
+    if t.is_contiguous():
         return width
-    if width > 1 and t.stride(-1) != 1:
+    stride = t.stride()
+    if width > 1 and stride[-1] != 1:
         raise ValueError(f"{name}: the last dimension must be dense")
     ld, inner = None, 1
-    for size, st in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+    for size, st in zip(shape[-2::-1], stride[-2::-1]):
         if size == 1:
             continue
         if ld is None:
             ld = st
         elif st != ld * inner:
-            raise ValueError(f"{name}: rows must lie at equal distances, got strides {t.stride()}")
+            raise ValueError(f"{name}: rows must lie at equal distances, got strides {stride}")
         inner *= size
     ld = width if ld is None else ld
     if ld < width:
-        raise ValueError(f"{name}: rows overlap, got strides {t.stride()}")
+        raise ValueError(f"{name}: rows overlap, got strides {stride}")
     return ld
 
 
+def _dims(name, t, n):
+    if t.dim() != n:
+        raise ValueError(f"{name} must have {n} dimensions, got shape {tuple(t.shape)}")
+    return t.shape
+
+
 class _Launch:
-    """Allocations of one call belong to the stream it launches on; when that is not the current
-    stream, the tensors it shares with the current one are recorded on both."""
+    """The stream a call launches on, and the call's allocations, which belong to that stream.  Where
+    it is not the current one, the tensors that the two share are recorded on both, so that memory
+    freed after the call is not handed out again too early."""
 
-    def __init__(self, stream):
+    __slots__ = ("device", "raw", "stream", "outputs")
+
+    def __init__(self, x, stream):
         import torch
 
-        self.current = torch.cuda.current_stream()
-        self.stream = self.current if stream is None else stream
-        self.other = self.stream.cuda_stream != self.current.cuda_stream
-        self.outputs = []
+        if not x.is_cuda:
+            raise ValueError("tensors must be CUDA tensors (use .cuda())")
+        index, current = x.get_device(), torch._C._cuda_getDevice()
+        if index != current:
+            raise ValueError(f"tensors are on {x.device}, the current device is cuda:{current}")
+        self.device = x.device
+        self.raw = torch._C._cuda_getCurrentRawStream(index)
+        self.stream = None  # set where the launch is not on the current stream
+        if stream is not None:
+            if stream.device.index != index:
+                raise ValueError(f"stream is on {stream.device}, the tensors on {x.device}")
+            if stream.cuda_stream != self.raw:
+                self.stream, self.raw, self.outputs = stream, stream.cuda_stream, []
 
-    def _empty(self, shape, dtype, device):
+    def empty(self, shape, dtype, output=True):
         import torch
 
-        if not self.other:
-            return torch.empty(shape, dtype=dtype, device=device)
+        if self.stream is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
         with torch.cuda.stream(self.stream):
-            return torch.empty(shape, dtype=dtype, device=device)
-
-    def out(self, like, shape, dtype):
-        t = self._empty(shape, dtype, like.device)
-        self.outputs.append(t)
+            t = torch.empty(shape, dtype=dtype, device=self.device)
+        if output:
+            self.outputs.append(t)
         return t
 
-    def workspace(self, like, nbytes):
+    def workspace(self, nbytes):
         import torch
 
-        return self._empty((nbytes,), torch.uint8, like.device) if nbytes else None
-
-    def ptr(self):
-        return ctypes.c_void_p(self.stream.cuda_stream)
+        return self.empty((nbytes,), torch.uint8, output=False) if nbytes else None
 
     def done(self, *given):
-        if self.other:
+        import torch
+
+        if self.stream is not None:
+            current = torch.cuda.current_stream()
             for t in self.outputs:
-                t.record_stream(self.current)
+                t.record_stream(current)
             for t in given:
                 if t is not None:
                     t.record_stream(self.stream)
-
-
-ACT_NONE, ACT_SILU = 0, 1
 
 
 def rwkv_causal_conv_forward(x, weight, bias=None, state_in=None, *, silu=False, return_state=False, stream=None,
@@ -595,21 +616,21 @@ def rwkv_causal_conv_forward(x, weight, bias=None, state_in=None, *, silu=False,
     last W-1 tokens [B,W-1,C] if ``return_state``."""
     import torch
 
-    _need_here(stream, x=x, weight=weight, bias=bias, state_in=state_in, out=out)
+    L, dev, dt = _Launch(x, stream), x.device, x.dtype
     code = _io_code("x", x)
-    B, T, C = x.shape
-    W = weight.shape[-1]
-    _dense("weight", weight, (C, W), torch.float32)
-    _dense("bias", bias, (C,), torch.float32)
-    _dense("state_in", state_in, (B, W - 1, C), x.dtype)
-    _dense("out", out, (B, T, C), x.dtype)
-    ldx = _rows("x", x, (B, T, C), x.dtype)
-    L = _Launch(stream)
-    y = L.out(x, (B, T, C), x.dtype) if out is None else out
-    st = L.out(x, (B, W - 1, C), x.dtype) if return_state else None
+    B, T, C = _dims("x", x, 3)
+    W = _dims("weight", weight, 2)[1]
+    _dense("weight", weight, (C, W), torch.float32, dev)
+    _dense("bias", bias, (C,), torch.float32, dev)
+    _dense("state_in", state_in, (B, W - 1, C), dt, dev)
+    _dense("out", out, (B, T, C), dt, dev)
+    ldx = _rows("x", x, (B, T, C), dt, dev)
+    y = L.empty((B, T, C), dt) if out is None else out
+    st = L.empty((B, W - 1, C), dt) if return_state and W > 0 else None
     _check("rwkv_causal_conv_forward",
-           lib().rwkv_causal_conv_forward(B, T, C, W, code, _ptr(weight), _ptr(bias), ACT_SILU if silu else ACT_NONE,
-                                          _ptr(x), ldx, _ptr(y), _ptr(state_in), _ptr(st), L.ptr()))
+           _fn("rwkv_causal_conv_forward")(B, T, C, W, code, _addr(weight), _addr(bias),
+                                           ACT_SILU if silu else ACT_NONE, _addr(x), ldx, _addr(y), _addr(state_in),
+                                           _addr(st), L.raw))
     L.done(x, weight, bias, state_in, out)
     return (y, st) if return_state else y
 
@@ -621,27 +642,27 @@ def rwkv_causal_conv_backward(x, weight, gy, bias=None, state_in=None, gstate_ou
     gbias is None where bias is."""
     import torch
 
-    _need_here(stream, x=x, weight=weight, gy=gy, bias=bias, state_in=state_in, gstate_out=gstate_out)
+    L, dev, dt = _Launch(x, stream), x.device, x.dtype
     code = _io_code("x", x)
-    B, T, C = x.shape
-    W = weight.shape[-1]
-    _dense("weight", weight, (C, W), torch.float32)
-    _dense("bias", bias, (C,), torch.float32)
-    _dense("gy", gy, (B, T, C), x.dtype)
-    _dense("state_in", state_in, (B, W - 1, C), x.dtype)
-    _dense("gstate_out", gstate_out, (B, W - 1, C), x.dtype)
-    ldx = _rows("x", x, (B, T, C), x.dtype)
-    h, L = lib(), _Launch(stream)
-    gx = L.out(x, (B, T, C), x.dtype)
-    gw = L.out(x, (C, W), torch.float32)
-    gb = L.out(x, (C,), torch.float32) if bias is not None else None
-    gs = L.out(x, (B, W - 1, C), x.dtype) if want_gstate_in else None
-    wsb = int(h.rwkv_causal_conv_backward_workspace_bytes(B, T, C, W))
-    ws = L.workspace(x, wsb)
+    B, T, C = _dims("x", x, 3)
+    W = _dims("weight", weight, 2)[1]
+    _dense("weight", weight, (C, W), torch.float32, dev)
+    _dense("bias", bias, (C,), torch.float32, dev)
+    _dense("gy", gy, (B, T, C), dt, dev)
+    _dense("state_in", state_in, (B, W - 1, C), dt, dev)
+    _dense("gstate_out", gstate_out, (B, W - 1, C), dt, dev)
+    ldx = _rows("x", x, (B, T, C), dt, dev)
+    gx = L.empty((B, T, C), dt)
+    gw = L.empty((C, W), torch.float32)
+    gb = L.empty((C,), torch.float32) if bias is not None else None
+    gs = L.empty((B, W - 1, C), dt) if want_gstate_in and W > 0 else None
+    wsb = _fn("rwkv_causal_conv_backward_workspace_bytes")(B, T, C, W)
+    ws = L.workspace(wsb)
     _check("rwkv_causal_conv_backward",
-           h.rwkv_causal_conv_backward(B, T, C, W, code, _ptr(weight), _ptr(bias), ACT_SILU if silu else ACT_NONE,
-                                       _ptr(x), ldx, _ptr(state_in), _ptr(gy), _ptr(gstate_out), _ptr(gx), _ptr(gw),
-                                       _ptr(gb), _ptr(gs), _ptr(ws), wsb, L.ptr()))
+           _fn("rwkv_causal_conv_backward")(B, T, C, W, code, _addr(weight), _addr(bias),
+                                            ACT_SILU if silu else ACT_NONE, _addr(x), ldx, _addr(state_in), _addr(gy),
+                                            _addr(gstate_out), _addr(gx), _addr(gw), _addr(gb), _addr(gs), _addr(ws),
+                                            wsb, L.raw))
     L.done(x, weight, gy, bias, state_in, gstate_out)
     return (gx, gw, gb, gs) if want_gstate_in else (gx, gw, gb)
 
@@ -651,38 +672,39 @@ def rwkv_causal_conv_step(x, weight, state, bias=None, *, silu=False, state_out=
     ``state_out`` is given.  Returns y [B,C]."""
     import torch
 
-    _need_here(stream, x=x, weight=weight, state=state, bias=bias, state_out=state_out, out=out)
+    L, dev, dt = _Launch(x, stream), x.device, x.dtype
     code = _io_code("x", x)
-    B, C = x.shape
-    W = weight.shape[-1]
-    _dense("weight", weight, (C, W), torch.float32)
-    _dense("bias", bias, (C,), torch.float32)
-    _dense("state", state, (B, W - 1, C), x.dtype)
-    _dense("state_out", state_out, (B, W - 1, C), x.dtype)
-    _dense("out", out, (B, C), x.dtype)
-    ldx = _rows("x", x, (B, C), x.dtype)
-    L = _Launch(stream)
-    y = L.out(x, (B, C), x.dtype) if out is None else out
+    B, C = _dims("x", x, 2)
+    W = _dims("weight", weight, 2)[1]
+    _dense("weight", weight, (C, W), torch.float32, dev)
+    _dense("bias", bias, (C,), torch.float32, dev)
+    _dense("state", state, (B, W - 1, C), dt, dev)
+    _dense("state_out", state_out, (B, W - 1, C), dt, dev)
+    _dense("out", out, (B, C), dt, dev)
+    ldx = _rows("x", x, (B, C), dt, dev)
+    y = L.empty((B, C), dt) if out is None else out
     so = state if state_out is None else state_out
     _check("rwkv_causal_conv_step",
-           lib().rwkv_causal_conv_step(B, C, W, code, _ptr(weight), _ptr(bias), ACT_SILU if silu else ACT_NONE,
-                                       _ptr(x), ldx, _ptr(y), _ptr(state), _ptr(so), L.ptr()))
+           _fn("rwkv_causal_conv_step")(B, C, W, code, _addr(weight), _addr(bias), ACT_SILU if silu else ACT_NONE,
+                                        _addr(x), ldx, _addr(y), _addr(state), _addr(so), L.raw))
     L.done(x, weight, state, bias, state_out, out)
     return y
 
 
 def _scan_args(x, dt, b, c, a_log, d, dt_bias, z):
-    """Checks what the scan's calls share; returns (N, the ld of x, dt, b, c and z)."""
+    """Checks what the scan's calls share; returns N and the C calls' arguments from a_log to ldz."""
     import torch
 
-    lead, C, N = tuple(x.shape[:-1]), x.shape[-1], a_log.shape[-1]
-    _dense("a_log", a_log, (C, N), torch.float32)
-    _dense("d", d, (C,), torch.float32)
-    _dense("dt_bias", dt_bias, (C,), torch.float32)
-    lds = [_rows("x", x, lead + (C,), x.dtype), _rows("dt", dt, lead + (C,), x.dtype),
-           _rows("b", b, lead + (N,), x.dtype), _rows("c", c, lead + (N,), x.dtype),
-           _rows("z", z, lead + (C,), x.dtype) if z is not None else C]
-    return N, lds
+    lead, C, dev, ty = x.shape[:-1], x.shape[-1], x.device, x.dtype
+    N = _dims("a_log", a_log, 2)[1]
+    _dense("a_log", a_log, (C, N), torch.float32, dev)
+    _dense("d", d, (C,), torch.float32, dev)
+    _dense("dt_bias", dt_bias, (C,), torch.float32, dev)
+    wide, state = lead + (C,), lead + (N,)
+    return N, (_addr(a_log), _addr(d), _addr(dt_bias),
+               _addr(x), _rows("x", x, wide, ty, dev), _addr(dt), _rows("dt", dt, wide, ty, dev),
+               _addr(b), _rows("b", b, state, ty, dev), _addr(c), _rows("c", c, state, ty, dev),
+               _addr(z), _rows("z", z, wide, ty, dev) if z is not None else C)
 
 
 def rwkv_selective_scan_forward(x, dt, b, c, a_log, d=None, dt_bias=None, z=None, h_in=None, *, return_state=False,
@@ -696,22 +718,20 @@ def rwkv_selective_scan_forward(x, dt, b, c, a_log, d=None, dt_bias=None, z=None
     ``rwkv_selective_scan_backward`` if ``checkpoints``."""
     import torch
 
-    _need_here(stream, x=x, dt=dt, b=b, c=c, a_log=a_log, d=d, dt_bias=dt_bias, z=z, h_in=h_in, out=out)
+    L, dev, ty = _Launch(x, stream), x.device, x.dtype
     code = _io_code("x", x)
-    B, T, C = x.shape
-    N, (ldx, lddt, ldb, ldc, ldz) = _scan_args(x, dt, b, c, a_log, d, dt_bias, z)
-    _dense("h_in", h_in, (B, C, N), torch.float32)
-    _dense("out", out, (B, T, C), x.dtype)
-    h, L = lib(), _Launch(stream)
-    y = L.out(x, (B, T, C), x.dtype) if out is None else out
-    ho = L.out(x, (B, C, N), torch.float32) if return_state else None
-    ck = L.out(x, ((T + CHUNK_LEN - 1) // CHUNK_LEN, B, C, N), torch.float32) if checkpoints else None
-    wsb = int(h.rwkv_selective_scan_forward_workspace_bytes(B, T, C, N, algo))
-    ws = L.workspace(x, wsb)
+    B, T, C = _dims("x", x, 3)
+    N, args = _scan_args(x, dt, b, c, a_log, d, dt_bias, z)
+    _dense("h_in", h_in, (B, C, N), torch.float32, dev)
+    _dense("out", out, (B, T, C), ty, dev)
+    y = L.empty((B, T, C), ty) if out is None else out
+    ho = L.empty((B, C, N), torch.float32) if return_state else None
+    ck = L.empty(((T + CHUNK_LEN - 1) // CHUNK_LEN, B, C, N), torch.float32) if checkpoints else None
+    wsb = _fn("rwkv_selective_scan_forward_workspace_bytes")(B, T, C, N, algo)
+    ws = L.workspace(wsb)
     _check("rwkv_selective_scan_forward",
-           h.rwkv_selective_scan_forward(B, T, C, N, code, _ptr(a_log), _ptr(d), _ptr(dt_bias), _ptr(x), ldx,
-                                         _ptr(dt), lddt, _ptr(b), ldb, _ptr(c), ldc, _ptr(z), ldz, _ptr(y),
-                                         _ptr(h_in), _ptr(ho), _ptr(ck), CHUNK_LEN, algo, _ptr(ws), wsb, L.ptr()))
+           _fn("rwkv_selective_scan_forward")(B, T, C, N, code, *args, _addr(y), _addr(h_in), _addr(ho), _addr(ck),
+                                              CHUNK_LEN, algo, _addr(ws), wsb, L.raw))
     L.done(x, dt, b, c, a_log, d, dt_bias, z, h_in, out)
     res = (y,)
     if return_state:
@@ -729,31 +749,29 @@ def rwkv_selective_scan_backward(x, dt, b, c, a_log, gy, d=None, dt_bias=None, z
     checkpoints, or None to form them again (from ``h_in``)."""
     import torch
 
-    _need_here(stream, x=x, dt=dt, b=b, c=c, a_log=a_log, gy=gy, d=d, dt_bias=dt_bias, z=z, ckpt=ckpt, h_in=h_in,
-               gh_out=gh_out)
+    L, dev, ty = _Launch(x, stream), x.device, x.dtype
     code = _io_code("x", x)
-    B, T, C = x.shape
-    N, (ldx, lddt, ldb, ldc, ldz) = _scan_args(x, dt, b, c, a_log, d, dt_bias, z)
-    _dense("gy", gy, (B, T, C), x.dtype)
-    _dense("ckpt", ckpt, ((T + CHUNK_LEN - 1) // CHUNK_LEN, B, C, N), torch.float32)
-    _dense("h_in", h_in, (B, C, N), torch.float32)
-    _dense("gh_out", gh_out, (B, C, N), torch.float32)
-    h, L = lib(), _Launch(stream)
-    gx, gdt = L.out(x, (B, T, C), x.dtype), L.out(x, (B, T, C), x.dtype)
-    gb, gc = L.out(x, (B, T, N), x.dtype), L.out(x, (B, T, N), x.dtype)
-    gz = L.out(x, (B, T, C), x.dtype) if z is not None else None
-    ga = L.out(x, (C, N), torch.float32)
-    gd = L.out(x, (C,), torch.float32) if d is not None else None
-    gbias = L.out(x, (C,), torch.float32) if dt_bias is not None else None
-    ghi = L.out(x, (B, C, N), torch.float32) if want_gh_in else None
-    wsb = int(h.rwkv_selective_scan_backward_workspace_bytes(B, T, C, N, CHUNK_LEN, 1 if ckpt is not None else 0))
-    ws = L.workspace(x, wsb)
+    B, T, C = _dims("x", x, 3)
+    N, args = _scan_args(x, dt, b, c, a_log, d, dt_bias, z)
+    f32 = torch.float32
+    _dense("gy", gy, (B, T, C), ty, dev)
+    _dense("ckpt", ckpt, ((T + CHUNK_LEN - 1) // CHUNK_LEN, B, C, N), f32, dev)
+    _dense("h_in", h_in, (B, C, N), f32, dev)
+    _dense("gh_out", gh_out, (B, C, N), f32, dev)
+    gx, gdt = L.empty((B, T, C), ty), L.empty((B, T, C), ty)
+    gb, gc = L.empty((B, T, N), ty), L.empty((B, T, N), ty)
+    gz = L.empty((B, T, C), ty) if z is not None else None
+    ga = L.empty((C, N), f32)
+    gd = L.empty((C,), f32) if d is not None else None
+    gbias = L.empty((C,), f32) if dt_bias is not None else None
+    ghi = L.empty((B, C, N), f32) if want_gh_in else None
+    wsb = _fn("rwkv_selective_scan_backward_workspace_bytes")(B, T, C, N, CHUNK_LEN, 1 if ckpt is not None else 0)
+    ws = L.workspace(wsb)
     _check("rwkv_selective_scan_backward",
-           h.rwkv_selective_scan_backward(B, T, C, N, code, _ptr(a_log), _ptr(d), _ptr(dt_bias), _ptr(x), ldx,
-                                          _ptr(dt), lddt, _ptr(b), ldb, _ptr(c), ldc, _ptr(z), ldz, _ptr(gy),
-                                          _ptr(h_in), _ptr(gh_out), _ptr(ckpt), CHUNK_LEN, _ptr(gx), _ptr(gdt),
-                                          _ptr(gb), _ptr(gc), _ptr(gz), _ptr(ga), _ptr(gd), _ptr(gbias), _ptr(ghi),
-                                          _ptr(ws), wsb, L.ptr()))
+           _fn("rwkv_selective_scan_backward")(B, T, C, N, code, *args, _addr(gy), _addr(h_in), _addr(gh_out),
+                                               _addr(ckpt), CHUNK_LEN, _addr(gx), _addr(gdt), _addr(gb), _addr(gc),
+                                               _addr(gz), _addr(ga), _addr(gd), _addr(gbias), _addr(ghi), _addr(ws),
+                                               wsb, L.raw))
     L.done(x, dt, b, c, a_log, gy, d, dt_bias, z, ckpt, h_in, gh_out)
     res = (gx, gdt, gb, gc, ga, gd, gbias, gz)
     return res + (ghi,) if want_gh_in else res
@@ -765,21 +783,17 @@ def rwkv_selective_scan_step(x, dt, b, c, a_log, state, d=None, dt_bias=None, z=
     place unless ``state_out`` is given.  Returns y [B,C]."""
     import torch
 
-    _need_here(stream, x=x, dt=dt, b=b, c=c, a_log=a_log, state=state, d=d, dt_bias=dt_bias, z=z,
-               state_out=state_out, out=out)
+    L, dev, ty = _Launch(x, stream), x.device, x.dtype
     code = _io_code("x", x)
-    B, C = x.shape
-    N, (ldx, lddt, ldb, ldc, ldz) = _scan_args(x, dt, b, c, a_log, d, dt_bias, z)
-    _dense("state", state, (B, C, N), torch.float32)
-    _dense("state_out", state_out, (B, C, N), torch.float32)
-    _dense("out", out, (B, C), x.dtype)
-    L = _Launch(stream)
-    y = L.out(x, (B, C), x.dtype) if out is None else out
+    B, C = _dims("x", x, 2)
+    N, args = _scan_args(x, dt, b, c, a_log, d, dt_bias, z)
+    _dense("state", state, (B, C, N), torch.float32, dev)
+    _dense("state_out", state_out, (B, C, N), torch.float32, dev)
+    _dense("out", out, (B, C), ty, dev)
+    y = L.empty((B, C), ty) if out is None else out
     so = state if state_out is None else state_out
     _check("rwkv_selective_scan_step",
-           lib().rwkv_selective_scan_step(B, C, N, code, _ptr(a_log), _ptr(d), _ptr(dt_bias), _ptr(x), ldx, _ptr(dt),
-                                          lddt, _ptr(b), ldb, _ptr(c), ldc, _ptr(z), ldz, _ptr(y), _ptr(state),
-                                          _ptr(so), L.ptr()))
+           _fn("rwkv_selective_scan_step")(B, C, N, code, *args, _addr(y), _addr(state), _addr(so), L.raw))
     L.done(x, dt, b, c, a_log, state, d, dt_bias, z, state_out, out)
     return y
 
@@ -788,13 +802,16 @@ def _norm_args(x, weight, bias, gate, groups):
     """Checks what the norm's calls share; returns (M, N) for `groups` groups in x's last dimension."""
     import torch
 
-    C = x.shape[-1]
+    shape, dev = x.shape, x.device
+    if len(shape) == 0:
+        raise ValueError("x must have at least one dimension")
+    C = shape[-1]
     if groups < 1 or C % groups != 0:
         raise ValueError(f"groups must divide the last dimension {C}, got {groups}")
-    _dense("x", x, x.shape, x.dtype)
-    _dense("weight", weight, (C,), torch.float32)
-    _dense("bias", bias, (C,), torch.float32)
-    _dense("gate", gate, x.shape, x.dtype)
+    _dense("x", x, shape, x.dtype, dev)
+    _dense("weight", weight, (C,), torch.float32, dev)
+    _dense("bias", bias, (C,), torch.float32, dev)
+    _dense("gate", gate, shape, x.dtype, dev)
     return (x.numel() // C if C else 0), C // groups
 
 
@@ -803,15 +820,14 @@ def rwkv_layer_norm_forward(x, weight, bias=None, gate=None, *, groups=1, eps=1e
     (x - mean) / sqrt(var + eps) * weight + bias, times silu(gate) if a gate (like x) is given.
     x fp32 or bf16; weight, bias [C] fp32.  groups = H on an Eagle or Finch output [B,T,H*64] is
     the head-wise norm."""
-    _need_here(stream, x=x, weight=weight, bias=bias, gate=gate, out=out)
+    L = _Launch(x, stream)
     code = _io_code("x", x)
     M, N = _norm_args(x, weight, bias, gate, groups)
-    _dense("out", out, x.shape, x.dtype)
-    L = _Launch(stream)
-    y = L.out(x, x.shape, x.dtype) if out is None else out
+    _dense("out", out, x.shape, x.dtype, x.device)
+    y = L.empty(x.shape, x.dtype) if out is None else out
     _check("rwkv_layer_norm_forward",
-           lib().rwkv_layer_norm_forward(M, groups, N, code, _ptr(weight), _ptr(bias), eps, _ptr(x), _ptr(gate),
-                                         _ptr(y), L.ptr()))
+           _fn("rwkv_layer_norm_forward")(M, groups, N, code, _addr(weight), _addr(bias), eps, _addr(x), _addr(gate),
+                                          _addr(y), L.raw))
     L.done(x, weight, bias, gate, out)
     return y
 
@@ -821,21 +837,21 @@ def rwkv_layer_norm_backward(x, weight, gy, bias=None, gate=None, *, groups=1, e
     gbias and ggate are None where bias and gate are."""
     import torch
 
-    _need_here(stream, x=x, weight=weight, gy=gy, bias=bias, gate=gate)
+    L = _Launch(x, stream)
     code = _io_code("x", x)
     M, N = _norm_args(x, weight, bias, gate, groups)
-    _dense("gy", gy, x.shape, x.dtype)
+    _dense("gy", gy, x.shape, x.dtype, x.device)
     C = x.shape[-1]
-    h, L = lib(), _Launch(stream)
-    gx = L.out(x, x.shape, x.dtype)
-    gw = L.out(x, (C,), torch.float32)
-    gb = L.out(x, (C,), torch.float32) if bias is not None else None
-    gg = L.out(x, x.shape, x.dtype) if gate is not None else None
-    wsb = int(h.rwkv_layer_norm_backward_workspace_bytes(M, groups, N, code))
-    ws = L.workspace(x, wsb)
+    gx = L.empty(x.shape, x.dtype)
+    gw = L.empty((C,), torch.float32)
+    gb = L.empty((C,), torch.float32) if bias is not None else None
+    gg = L.empty(x.shape, x.dtype) if gate is not None else None
+    wsb = _fn("rwkv_layer_norm_backward_workspace_bytes")(M, groups, N, code)
+    ws = L.workspace(wsb)
     _check("rwkv_layer_norm_backward",
-           h.rwkv_layer_norm_backward(M, groups, N, code, _ptr(weight), _ptr(bias), eps, _ptr(x), _ptr(gate),
-                                      _ptr(gy), _ptr(gx), _ptr(gg), _ptr(gw), _ptr(gb), _ptr(ws), wsb, L.ptr()))
+           _fn("rwkv_layer_norm_backward")(M, groups, N, code, _addr(weight), _addr(bias), eps, _addr(x), _addr(gate),
+                                           _addr(gy), _addr(gx), _addr(gg), _addr(gw), _addr(gb), _addr(ws), wsb,
+                                           L.raw))
     L.done(x, weight, gy, bias, gate)
     return gx, gw, gb, gg
 

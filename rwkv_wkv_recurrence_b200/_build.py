@@ -52,7 +52,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
            "-I", os.path.join(ROOT, "include"), "-o", tmp]
     if ptxas_info:
         cmd += ["-Xptxas", "-v"]
-    cmd += [os.path.join(CSRC, s) for s in SOURCES]
+    cmd += ["-t", "0"] + [os.path.join(CSRC, s) for s in SOURCES]
     if verbose:
         print(" ".join(cmd), file=sys.stderr)
     subprocess.check_call(cmd, cwd=CSRC)

@@ -207,9 +207,26 @@ ScanPlan plan_scan_fwd(int64_t B, int64_t T, int64_t C, int64_t N, int algo) {
   const int64_t ch = scan_fwd_channels((int)N);
   return plan_scan(B * ((C + ch - 1) / ch), T, algo, 8);
 }
+// The backward's segments: the cost of a plan is the number of turns in which its CTAs pass through
+// the SMs (three at a time) times a segment's length; segments also take a pass of their own before
+// (the reversed recurrence, about a quarter of the main pass).
 ScanPlan plan_scan_bwd(int64_t B, int64_t T, int64_t C, int64_t N) {
-  const int64_t ch = scan_bwd_channels((int)N);
-  return plan_scan(B * ((C + ch - 1) / ch), T, RWKV_ALGO_AUTO, 2);
+  const int64_t ch = scan_bwd_channels((int)N), tiles = B * ((C + ch - 1) / ch), tile = scan_tile_tokens();
+  constexpr int64_t kSlots = 3 * kDesignSMs;
+  ScanPlan best;
+  double cost = 1e30;
+  for (int64_t k = 1; k <= 64; ++k) {
+    const int64_t len = ((T + k - 1) / k + tile - 1) / tile * tile;
+    if (k > 1 && len < 2 * tile) break;
+    const int64_t n = (T + len - 1) / len, turns = (tiles * n + kSlots - 1) / kSlots;
+    const double c = (double)turns * (double)len * (n > 1 ? 1.25 : 1.0);
+    if (c < cost * 0.999) {
+      cost = c;
+      best.seg_len = (int)std::min<int64_t>(len, INT_MAX / tile * tile);
+      best.nseg = (int)n;
+    }
+  }
+  return best;
 }
 
 struct ScanFwdWs {

@@ -287,6 +287,9 @@ int scan_fwd_channels(int N);  // channels per CTA
 int scan_bwd_channels(int N);
 int scan_tile_tokens();
 cudaError_t launch_scan_fwd(bool bf16, const ScanParams& p, cudaStream_t st);
+// The backward's recurrence over segments 1 .. nseg-1, each from zero at its end (the last from
+// gh_out): x = gy, b = c, h_in = gh_out, seg_h, seg_h0, seg_dt its workspace.
+cudaError_t launch_scan_reverse(bool bf16, const ScanParams& p, cudaStream_t st);
 cudaError_t launch_scan_bwd(bool bf16, const ScanBwdParams& p, cudaStream_t st);
 cudaError_t launch_scan_step(bool bf16, const ScanParams& p, cudaStream_t st);
 

@@ -96,6 +96,52 @@ __device__ __forceinline__ void store_part(T* p, int n, bool vec, const float (&
   }
 }
 
+// V elements as loaded, kept for later: unpacking them only where they are used leaves the load in
+// flight until then.
+template <typename T, int V>
+struct Raw {
+  static constexpr int kBytes = V * (int)sizeof(T);
+  uint32_t w[(kBytes + 3) / 4];
+
+  // The first n of the V elements at p (the rest zero); `vec` as in load_part.
+  __device__ __forceinline__ void load(const T* p, int n, bool vec) {
+    if (vec && n >= V) {
+      if constexpr (kBytes % 16 == 0) {
+#pragma unroll
+        for (int i = 0; i < kBytes / 16; ++i) {
+          const uint4 x = reinterpret_cast<const uint4*>(p)[i];
+          w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
+        }
+      } else if constexpr (kBytes == 8) {
+        const uint2 x = *reinterpret_cast<const uint2*>(p);
+        w[0] = x.x, w[1] = x.y;
+      } else if constexpr (kBytes == 4) {
+        w[0] = *reinterpret_cast<const uint32_t*>(p);
+      } else {
+        static_assert(kBytes == 2, "vector width");
+        w[0] = *reinterpret_cast<const unsigned short*>(p);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < (kBytes + 3) / 4; ++i) w[i] = 0u;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        if (i >= n) continue;
+        if constexpr (sizeof(T) == 4)
+          w[i] = reinterpret_cast<const uint32_t*>(p)[i];
+        else
+          w[i / 2] |= (uint32_t) reinterpret_cast<const unsigned short*>(p)[i] << (16 * (i & 1));
+      }
+    }
+  }
+  __device__ __forceinline__ float operator[](int i) const {
+    if constexpr (sizeof(T) == 4)
+      return __uint_as_float(w[i]);
+    else
+      return __uint_as_float((i & 1) != 0 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+  }
+};
+
 // softplus(v) = log(1 + e^v) = max(v, 0) + log1p(e^-|v|) and its derivative, the logistic sigmoid;
 // both keep their relative accuracy for very negative v, where the step sizes of a scan lie.
 __device__ __forceinline__ float softplus(float v, float& sig) {

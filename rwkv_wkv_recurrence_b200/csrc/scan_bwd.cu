@@ -6,75 +6,128 @@
 //   gx_t = Δ_t s1_t + d g_t,   gdt_t = σ(dt_t + dt_bias) (x_t s1_t + s2_t),   gdt_bias = Σ gdt,
 //   ga_log = A Σ q_t Δ_t,   gd = Σ g_t x_t,   gz_t = gy_t p_t silu'(z_t),   gh_in = e_0 G_0.
 //
-// The states come from the forward's checkpoints, one every 16 tokens.  A CTA of 256 threads owns
-// 1024/N channels (4 states of one channel per thread) and walks its time segment backwards, a
-// 16-token tile at a time: the states are recomputed forward from the checkpoint, 8 tokens at a
-// time with e_t and e_t h_{t-1} kept in registers (64 floats), then walked backwards with G.  The
-// first 8 tokens of a tile are so computed twice; keeping all 16 would take 128 registers, a
-// checkpoint every 8 tokens twice their bytes.
+// The states come from the forward's checkpoints, one every 16 tokens; a CTA owns 512/N channels and
+// walks its time segment backwards, a 16-token tile at a time: the states are run forward from the
+// checkpoint and kept every 4 tokens; then, from the last 4 tokens to the first, the 4 states and
+// decays are formed again in registers and walked backwards with G.
 //
-// Sums over a channel's states (p, s1, s2) fold four tokens at a time over its lanes.  Sums over
-// channels (gB, gC: B and C are shared by all of them) fold over the lanes of a warp, meet in
-// shared memory per CTA and go to the workspace per CTA; a last kernel adds the CTAs' parts.  No
-// atomics: the same inputs give the same bits.
+// What bounds it: the shared-memory pipe and the issue slots.  Every lane needs B_t[n] and C_t[n] of
+// its states, and a load costs that pipe 4 bytes a lane and turn even where all lanes read the same
+// words, so a thread owns 4 states of TWO channels and each loaded word serves both (one channel per
+// thread needed 9.3 turns per state and token, two 6).  N/4 neighbouring lanes own a channel pair.
+//   - Sums over a pair's states (p, s1, s2): half of a pair's lanes hold its two channels in the
+//     other order, so the first exchange gives away one channel and keeps the other without selects.
+//   - Sums over channels (gB, gC: all channels share B and C): the lanes hold their 4 states in an
+//     order XORed with their place in the warp (B and C lie in shared memory in each of the 4
+//     orders), so that the exchanges need no selects either; warps meet in shared memory, CTAs in the
+//     workspace, added by a last kernel.  No atomics: the same inputs give the same bits.
+//   - x, dt, z, gy and the checkpoint arrive by cp.async, a tile ahead, each thread reading back what
+//     it fetched.
 //
-// Few channels: time segments, as in the forward.  The carry G that enters a segment from behind
-// is folded from the later segments' own (each from zero, by a first launch) and their ΣΔ.
+// Time is cut into segments so that the CTAs fill the SMs evenly; the carry G that enters a segment
+// from behind is folded from the later segments' own (each from zero, by a first launch of
+// scan_fwd.cu's kernel in reverse) and their ΣΔ.
 #include "launch.h"
 #include "scan_common.cuh"
 
 namespace rwkv {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kTile = kScanCkLen;  // tokens per tile
-constexpr int kSub = 8;            // tokens whose states are in registers at once
-constexpr int kSN = 4;             // states per thread
+constexpr int kSub = 4;            // tokens whose states are in registers at once
+constexpr int kSN = 4;             // states per thread and channel
 constexpr float kLn2 = 0.693147180559945309f;
 
 template <int N>
 struct Shape {
-  static constexpr int kLanes = N / kSN;
-  static constexpr int kCh = kThreads / kLanes;           // channels per CTA
-  static constexpr int kChWarp = 32 / kLanes;             // channels per warp
-  static constexpr int kTokThreads = kThreads / kTile;    // threads per token in the tile's loads
-  static constexpr int kRun = kCh / kTokThreads;          // channels per thread there
+  static constexpr int kLanes = N / kSN;                // lanes per channel pair
+  static constexpr int kPairs = 32 / kLanes;            // channel pairs per warp
+  static constexpr int kCh = 2 * kPairs * kWarps;       // channels per CTA
+  static constexpr int kTokThreads = kThreads / kTile;  // threads per token in the tile's loads
+  static constexpr int kRun = kCh / kTokThreads;        // channels per thread there
+  static constexpr int kQuads = 2 * kTile * N / 4;      // groups of 4 states of B, then of C, in a tile
+  // column of channel ch in the (Δ, Δx, g, x) rows: the runs' stores fall on different banks
+  __device__ __forceinline__ static int col(int ch) {
+    constexpr int M = kRun < 8 ? kRun : 8;
+    return ch ^ ((ch / kRun) & (M - 1));
+  }
 };
 
-template <int N>
+// A run of elements that a thread fetches into shared memory for itself: pieces of up to 16 bytes,
+// piece k of thread tid at (k kThreads + tid) pieces.
+template <typename T, int RUN>
+struct Stage {
+  static constexpr int kBytes = RUN * (int)sizeof(T);
+  static constexpr int kPiece = kBytes < 16 ? kBytes : 16;
+  static constexpr int kElems = kPiece / (int)sizeof(T);
+  static constexpr int kPieces = kBytes / kPiece;
+  unsigned char raw[kPieces * kThreads * kPiece];
+
+  __device__ __forceinline__ void fetch(const T* src, int n, bool vec) {
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k) {
+      T* dst = reinterpret_cast<T*>(raw + (k * kThreads + threadIdx.x) * kPiece);
+      if (vec && n >= RUN) {
+        const uint32_t d = smem_u32(dst);
+        if constexpr (kPiece == 16)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src + k * kElems) : "memory");
+        else
+          asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(d), "l"(src + k * kElems), "n"(kPiece)
+                       : "memory");
+      } else {
+#pragma unroll
+        for (int e = 0; e < kElems; ++e)
+          dst[e] = k * kElems + e < n ? src[k * kElems + e] : IO<T>::from_f(0.f);
+      }
+    }
+  }
+  // Elements i and i + 1 (i even).
+  __device__ __forceinline__ float2 pair(int i) const {
+    const T* p = reinterpret_cast<const T*>(raw + (i / kElems * kThreads + threadIdx.x) * kPiece) + i % kElems;
+    float f[2];
+    if constexpr (kElems >= 2) {
+      load_vec<T, 2>(p, f);
+    } else {
+      f[0] = IO<T>::to_f(p[0]);
+      f[1] = IO<T>::to_f(*reinterpret_cast<const T*>(raw + ((i + 1) * kThreads + threadIdx.x) * kPiece));
+    }
+    return make_float2(f[0], f[1]);
+  }
+};
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+
+template <typename T, int N>
 struct __align__(16) Smem {
-  float4 dxg[kTile][Shape<N>::kCh];  // (Δ, Δ x, g, -)
-  float b[kTile][N], c[kTile][N];
-  float sum[3][kTile][Shape<N>::kCh + 8];  // Σ_n C h, Σ_n G B, Σ_n q A log2 e
-  float red[kWarps][kTile][2 * N];         // per warp: gC, gB of a token
+  using S = Shape<N>;
+  float4 dxg[kTile][S::kCh];              // (Δ, Δ x, g, x), then (gx, gdt / σ, p, -); columns permuted
+  float bc[2][kTile][4][N];               // B and C: copy p holds state 4 s + i at 4 s + (i ^ p)
+  float red[kWarps][kTile][2 * N];        // per warp: gC, gB of a token
+  float2 sg[S::kRun][kThreads];           // σ(dt + bias), gy silu'(z): each thread's own
+  float4 snap[kTile / kSub][2][kThreads]; // states before tokens 0, 4, 8, 12, each thread's own
+  Stage<T, S::kRun> x, dt, z, gy;
 };
 
-template <typename T, int N>
-struct Tile {
-  float x[Shape<N>::kRun], dt[Shape<N>::kRun], z[Shape<N>::kRun], gy[Shape<N>::kRun];
-};
-
-template <typename T, int N>
-__device__ __forceinline__ void load_tile(Tile<T, N>& R, const ScanBwdParams& p, int bb, int t, int t1, int c0,
-                                          int nc) {
-  constexpr int RUN = Shape<N>::kRun;
-  const ScanParams& f = p.f;
-  const bool ok = t < t1;
-  const size_t row = (size_t)bb * f.T + (ok ? t : 0);
-  const int n = ok ? nc : 0;
-  load_part<T, RUN>(static_cast<const T*>(f.x) + row * f.ldx + c0, n, f.vec, R.x);
-  load_part<T, RUN>(static_cast<const T*>(f.dt) + row * f.lddt + c0, n, f.vec, R.dt);
-  load_part<T, RUN>(static_cast<const T*>(p.gy) + row * f.C + c0, n, f.vec, R.gy);
-  if (f.z != nullptr) load_part<T, RUN>(static_cast<const T*>(f.z) + row * f.ldz + c0, n, f.vec, R.z);
+// v[i ^ p] of 4 states held as two pairs, p the lane's order.
+__device__ __forceinline__ void xor_order(float2 (&v)[2], int p) {
+  if (p & 2) {
+    const float2 t = v[0];
+    v[0] = v[1], v[1] = t;
+  }
+  if (p & 1) {
+    v[0] = make_float2(v[0].y, v[0].x);
+    v[1] = make_float2(v[1].y, v[1].x);
+  }
 }
 
 template <typename T, int N>
-__global__ void __launch_bounds__(kThreads) scan_bwd_kernel(const __grid_constant__ ScanBwdParams p) {
+__global__ void __launch_bounds__(kThreads, 3) scan_bwd_kernel(const __grid_constant__ ScanBwdParams p) {
   using S = Shape<N>;
-  constexpr int L = S::kLanes, CH = S::kCh, CW = S::kChWarp, RUN = S::kRun, TT = S::kTokThreads;
+  constexpr int L = S::kLanes, CP = S::kPairs, CH = S::kCh, RUN = S::kRun, TT = S::kTokThreads;
   extern __shared__ __align__(16) unsigned char raw[];
-  Smem<N>& sm = *reinterpret_cast<Smem<N>*>(raw);
+  Smem<T, N>& sm = *reinterpret_cast<Smem<T, N>*>(raw);
   const ScanParams& f = p.f;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int ct = (int)(blockIdx.x % (unsigned)f.ctiles);
@@ -82,166 +135,270 @@ __global__ void __launch_bounds__(kThreads) scan_bwd_kernel(const __grid_constan
   const int seg = (int)(rest % (unsigned)f.nseg), bb = (int)(rest / (unsigned)f.nseg);
   const int t0 = seg * f.seg_len, t1 = min(f.T, t0 + f.seg_len);
 
-  const int ch = tid / L, sub = tid % L;
-  const int c = ct * CH + ch;
-  const bool cact = c < f.C;
-  const size_t hoff = ((size_t)bb * f.C + c) * N + sub * kSN;
+  // the scan's view: 4 states, in the order i ^ ord, of channels ch[0] and ch[1]
+  const int sub = lane % L, cl = lane / L;
+  const int ord = CP >= 4 ? cl & 3 : (cl & 1) * 2;
+  const int swap = sub / (L / 2);  // the upper half of a pair's lanes holds its channels swapped
+  const int ch[2] = {(warp * CP + cl) * 2 + swap, (warp * CP + cl) * 2 + 1 - swap};
+  const int col[2] = {S::col(ch[0]), S::col(ch[1])};
   const size_t plane = (size_t)f.B * f.C * N;
-  float a2[kSN], gh[kSN], ga[kSN];
+  size_t hoff[2];
+  bool cact[2];
+  float2 a2[2][2], gh[2][2], ga[2][2];  // [channel][pair of states]
 #pragma unroll
-  for (int i = 0; i < kSN; ++i) a2[i] = gh[i] = ga[i] = 0.f;
-  if (cact) {
-    load_rates<kSN>(f.a_log + (size_t)c * N + sub * kSN, a2);
-    if (seg < f.nseg - 1) {  // the last segment's own gradient starts from gh_out
-      load_vec<float, kSN>(p.seg_g + (size_t)(f.nseg - 1) * plane + hoff, gh);
-      for (int s = f.nseg - 2; s > seg; --s) {
-        float x[kSN];
-        load_vec<float, kSN>(p.seg_g + (size_t)s * plane + hoff, x);
-        const float sd = p.seg_dt[((size_t)s * f.B + bb) * f.C + c];
+  for (int j = 0; j < 2; ++j) {
+    const int c = ct * CH + ch[j];
+    cact[j] = c < f.C;
+    hoff[j] = ((size_t)bb * f.C + (cact[j] ? c : 0)) * N + sub * kSN;
+    float r[kSN] = {0.f, 0.f, 0.f, 0.f};
+    if (cact[j]) load_rates<kSN>(f.a_log + (size_t)c * N + sub * kSN, r);
 #pragma unroll
-        for (int i = 0; i < kSN; ++i) gh[i] = fmaf(ex2(sd * a2[i]), gh[i], x[i]);
-      }
-    } else if (p.gh_out != nullptr) {
-      // a copy when segmented: gh_in may be the same array, and another CTA writes it
-      load_vec<float, kSN>((f.nseg > 1 ? p.seg_g0 : p.gh_out) + hoff, gh);
+    for (int q = 0; q < 2; ++q) {
+      a2[j][q] = make_float2(r[2 * q], r[2 * q + 1]);
+      gh[j][q] = ga[j][q] = dup2(0.f);
     }
+    if (cact[j]) {
+      if (seg < f.nseg - 1) {  // the last segment's own gradient starts from gh_out
+        load_pairs<2>(p.seg_g + (size_t)(f.nseg - 1) * plane + hoff[j], gh[j]);
+        for (int s = f.nseg - 2; s > seg; --s) {
+          float2 x[2];
+          load_pairs<2>(p.seg_g + (size_t)s * plane + hoff[j], x);
+          const float2 sd = dup2(p.seg_dt[((size_t)s * f.B + bb) * f.C + c]);
+#pragma unroll
+          for (int q = 0; q < 2; ++q) gh[j][q] = fma2(ex2_2(mul2(sd, a2[j][q])), gh[j][q], x[q]);
+        }
+      } else if (p.gh_out != nullptr) {
+        // a copy when segmented: gh_in may be the same array, and another CTA writes it
+        load_pairs<2>((f.nseg > 1 ? p.seg_g0 : p.gh_out) + hoff[j], gh[j]);
+      }
+    }
+    xor_order(a2[j], ord);
+    xor_order(gh[j], ord);
   }
 
+  const float dsk = f.d != nullptr && cact[0] ? f.d[ct * CH + ch[0]] : 0.f;
+
+  // the loads' view: one token of the tile, a run of channels
   const int lt = tid / TT, lq = tid % TT;
   const int c0 = ct * CH + lq * RUN, nc = max(0, min(RUN, f.C - c0));
-  float bias[RUN], dsk[RUN], gd[RUN], gbias[RUN];
+  float gd[RUN], gbias[RUN];
 #pragma unroll
-  for (int i = 0; i < RUN; ++i) {
-    bias[i] = f.dt_bias != nullptr && i < nc ? f.dt_bias[c0 + i] : 0.f;
-    dsk[i] = f.d != nullptr && i < nc ? f.d[c0 + i] : 0.f;
-    gd[i] = gbias[i] = 0.f;
-  }
-  Tile<T, N> R;
+  for (int i = 0; i < RUN; ++i) gd[i] = gbias[i] = 0.f;
+
+  constexpr int QT = (S::kQuads + kThreads - 1) / kThreads;
+  Raw<T, 4> bc[QT];
+  const auto fetch = [&](int ts) {  // a tile's inputs, on their way
+    const bool ok = ts + lt < t1;
+    const size_t row = (size_t)bb * f.T + (ok ? ts + lt : 0);
+    const int n = ok ? nc : 0;
+    sm.x.fetch(static_cast<const T*>(f.x) + row * f.ldx + c0, n, f.vec);
+    sm.dt.fetch(static_cast<const T*>(f.dt) + row * f.lddt + c0, n, f.vec);
+    sm.gy.fetch(static_cast<const T*>(p.gy) + row * f.C + c0, n, f.vec);
+    if (f.z != nullptr) sm.z.fetch(static_cast<const T*>(f.z) + row * f.ldz + c0, n, f.vec);
+    cp_async_commit();
+#pragma unroll
+    for (int k = 0; k < QT; ++k) {
+      const int id = tid + k * kThreads;
+      if (S::kQuads % kThreads != 0 && id >= S::kQuads) continue;
+      const bool is_c = id >= S::kQuads / 2;
+      const int qi = is_c ? id - S::kQuads / 2 : id, tk = ts + qi / (N / 4), s0 = qi % (N / 4) * 4;
+      const bool on = tk < t1;
+      const size_t rq = (size_t)bb * f.T + (on ? tk : 0);
+      bc[k].load(static_cast<const T*>(is_c ? f.c : f.b) + rq * (is_c ? f.ldc : f.ldb) + s0, on ? 4 : 0, f.vec_bc);
+    }
+  };
+  const auto fetch_state = [&](int ts) {  // the states before token ts, into this thread's first snapshot
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      float4* dst = &sm.snap[0][j][tid];
+      if (cact[j])
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)),
+                     "l"(f.ckpt + (size_t)(ts / kScanCkLen) * plane + hoff[j])
+                     : "memory");
+      else
+        *dst = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    cp_async_commit();
+  };
   int ts = t0 + (t1 - t0 - 1) / kTile * kTile;
-  load_tile<T, N>(R, p, bb, ts + lt, t1, c0, nc);
+  fetch(ts);
+  fetch_state(ts);
 
   for (; ts >= t0; ts -= kTile) {
     const bool tact = ts + lt < t1;
-    float sig[RUN], x[RUN], gpre[RUN];  // σ(dt + bias); x; gy silu'(z)
+    cp_async_wait_all();
 #pragma unroll
-    for (int i = 0; i < RUN; ++i) {
-      const bool on = tact && i < nc;
-      float delta = softplus(R.dt[i] + bias[i], sig[i]);
-      float g = R.gy[i];
-      x[i] = R.x[i];
-      gpre[i] = 0.f;
-      if (f.z != nullptr) {
-        const float s = sigmoid(R.z[i]);
-        gpre[i] = g * s * fmaf(R.z[i], 1.f - s, 1.f);
-        g *= R.z[i] * s;
+    for (int i = 0; i < RUN; i += 2) {
+      float2 v = sm.dt.pair(i), g = sm.gy.pair(i), e;
+      const float2 x = sm.x.pair(i);
+      if (f.dt_bias != nullptr) {
+        if (i < nc) v.x += f.dt_bias[c0 + i];
+        if (i + 1 < nc) v.y += f.dt_bias[c0 + i + 1];
       }
-      sm.dxg[lt][lq * RUN + i] = on ? make_float4(delta, delta * x[i], g, 0.f) : make_float4(0.f, 0.f, 0.f, 0.f);
-      if (on) gd[i] = fmaf(g, x[i], gd[i]);
+      const float2 dl = softplus2(v, e);
+      const float rx = rcp_approx(1.f + e.x), ry = rcp_approx(1.f + e.y);
+      float2 sig = make_float2(v.x >= 0.f ? rx : e.x * rx, v.y >= 0.f ? ry : e.y * ry);
+      float2 gpre = dup2(0.f);  // gy silu'(z)
+      if (f.z != nullptr) {
+        const float2 z = sm.z.pair(i);
+        const float sx = sigmoid(z.x), sy = sigmoid(z.y);
+        gpre = make_float2(g.x * sx * fmaf(z.x, 1.f - sx, 1.f), g.y * sy * fmaf(z.y, 1.f - sy, 1.f));
+        g = make_float2(g.x * (z.x * sx), g.y * (z.y * sy));
+      }
+      const bool on0 = tact && i < nc, on1 = tact && i + 1 < nc;
+      const int cc = lq * RUN + i;
+      sm.dxg[lt][S::col(cc)] = on0 ? make_float4(dl.x, dl.x * x.x, g.x, x.x) : make_float4(0.f, 0.f, 0.f, 0.f);
+      sm.dxg[lt][S::col(cc + 1)] = on1 ? make_float4(dl.y, dl.y * x.y, g.y, x.y) : make_float4(0.f, 0.f, 0.f, 0.f);
+      sm.sg[i][tid] = make_float2(sig.x, gpre.x);
+      sm.sg[i + 1][tid] = make_float2(sig.y, gpre.y);
+      if (on0) gd[i] = fmaf(g.x, x.x, gd[i]);
+      if (on1) gd[i + 1] = fmaf(g.y, x.y, gd[i + 1]);
     }
-    for (int i = tid; i < kTile * N; i += kThreads) {
-      const int tk = i / N, n = i % N;
-      const bool ok = ts + tk < t1;
-      const size_t row = (size_t)bb * f.T + (ok ? ts + tk : 0);
-      sm.b[tk][n] = ok ? IO<T>::to_f(static_cast<const T*>(f.b)[row * f.ldb + n]) : 0.f;
-      sm.c[tk][n] = ok ? IO<T>::to_f(static_cast<const T*>(f.c)[row * f.ldc + n]) : 0.f;
+#pragma unroll
+    for (int k = 0; k < QT; ++k) {
+      const int id = tid + k * kThreads;
+      if (S::kQuads % kThreads != 0 && id >= S::kQuads) continue;
+      const int which = id >= S::kQuads / 2, qi = which ? id - S::kQuads / 2 : id;
+      float* dst = &sm.bc[which][qi / (N / 4)][0][qi % (N / 4) * 4];
+      const float a = bc[k][0], b = bc[k][1], c = bc[k][2], d = bc[k][3];
+      *reinterpret_cast<float4*>(dst) = make_float4(a, b, c, d);
+      *reinterpret_cast<float4*>(dst + N) = make_float4(b, a, d, c);
+      *reinterpret_cast<float4*>(dst + 2 * N) = make_float4(c, d, a, b);
+      *reinterpret_cast<float4*>(dst + 3 * N) = make_float4(d, c, b, a);
     }
-    float h0[kSN] = {0.f, 0.f, 0.f, 0.f};
-    if (cact) load_vec<float, kSN>(f.ckpt + (size_t)(ts / kScanCkLen) * plane + hoff, h0);
-    if (ts > t0) load_tile<T, N>(R, p, bb, ts - kTile + lt, t1, c0, nc);
+    float2 h[2][2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const float4 v = sm.snap[0][j][tid];
+      h[j][0] = make_float2(v.x, v.y), h[j][1] = make_float2(v.z, v.w);
+      xor_order(h[j], ord);
+    }
+    if (ts > t0) fetch(ts - kTile);
     __syncthreads();
 
-    float h[kSN];
+    // the states every 4 tokens
+#pragma unroll 4
+    for (int k = 0; k < kTile; ++k) {
+      if (k % kSub == 0) {  // in the lane's order (the first, as fetched, too)
 #pragma unroll
-    for (int i = 0; i < kSN; ++i) h[i] = h0[i];
+        for (int j = 0; j < 2; ++j) store_pairs<2>(reinterpret_cast<float*>(&sm.snap[k / kSub][j][tid]), h[j]);
+        if (k == kTile - kSub) break;
+      }
+      float2 bv[2];
+      load_pairs<2>(&sm.bc[0][k][ord][sub * kSN], bv);
 #pragma unroll
-    for (int k = 0; k < kSub; ++k) {
-      const float4 d = sm.dxg[k][ch];
-      float bv[kSN];
-      load_vec<float, kSN>(&sm.b[k][sub * kSN], bv);
+      for (int j = 0; j < 2; ++j) {
+        const float2 d = *reinterpret_cast<const float2*>(&sm.dxg[k][col[j]]);
 #pragma unroll
-      for (int i = 0; i < kSN; ++i) h[i] = fmaf(ex2(d.x * a2[i]), h[i], d.y * bv[i]);
+        for (int q = 0; q < 2; ++q)
+          h[j][q] = fma2(ex2_2(mul2(dup2(d.x), a2[j][q])), h[j][q], mul2(dup2(d.y), bv[q]));
+      }
     }
+
 #pragma unroll 1
-    for (int half = 1; half >= 0; --half) {
-      const int s0 = half * kSub;
-      float e[kSub][kSN], eh[kSub][kSN];  // e_t, e_t h_{t-1}
+    for (int sb = kTile / kSub - 1; sb >= 0; --sb) {
+      const int k0 = sb * kSub;
+      float2 hh[kSub + 1][2][2], e[kSub][2][2];  // states before each token and after the last; decays
+#pragma unroll
+      for (int j = 0; j < 2; ++j) load_pairs<2>(reinterpret_cast<const float*>(&sm.snap[sb][j][tid]), hh[0][j]);
 #pragma unroll
       for (int k = 0; k < kSub; ++k) {
-        const float4 d = sm.dxg[s0 + k][ch];
-        float bv[kSN];
-        load_vec<float, kSN>(&sm.b[s0 + k][sub * kSN], bv);
+        float2 bv[2];
+        load_pairs<2>(&sm.bc[0][k0 + k][ord][sub * kSN], bv);
 #pragma unroll
-        for (int i = 0; i < kSN; ++i) {
-          e[k][i] = ex2(d.x * a2[i]);
-          eh[k][i] = e[k][i] * h[i];
-          h[i] = fmaf(d.y, bv[i], eh[k][i]);
-        }
-      }
+        for (int j = 0; j < 2; ++j) {
+          const float2 d = *reinterpret_cast<const float2*>(&sm.dxg[k0 + k][col[j]]);
 #pragma unroll
-      for (int grp = kSub - 4; grp >= 0; grp -= 4) {
-        float sp[4], s1[4], s2[4];
-#pragma unroll
-        for (int kk = 3; kk >= 0; --kk) {
-          const int k = grp + kk;
-          const float4 d = sm.dxg[s0 + k][ch];
-          float bv[kSN], cv[kSN], v[2 * kSN];
-          load_vec<float, kSN>(&sm.b[s0 + k][sub * kSN], bv);
-          load_vec<float, kSN>(&sm.c[s0 + k][sub * kSN], cv);
-          sp[kk] = s1[kk] = s2[kk] = 0.f;
-#pragma unroll
-          for (int i = 0; i < kSN; ++i) {
-            const float ht = fmaf(d.y, bv[i], eh[k][i]);
-            gh[i] = fmaf(cv[i], d.z, gh[i]);
-            sp[kk] = fmaf(cv[i], ht, sp[kk]);
-            s1[kk] = fmaf(gh[i], bv[i], s1[kk]);
-            v[i] = d.z * ht;
-            v[kSN + i] = d.y * gh[i];
-            const float q = gh[i] * eh[k][i];
-            s2[kk] = fmaf(q, a2[i], s2[kk]);
-            ga[i] = fmaf(q, d.x, ga[i]);
-            gh[i] *= e[k][i];
-          }
-          constexpr int M = CW < 8 ? CW : 8;  // lanes with different sums
-          const int idx = lane / L;
-          fold_lanes<2 * kSN, CW, L>(v, idx);
-          if (idx < M) {
-#pragma unroll
-            for (int j = 0; j < 8 / M; ++j) {
-              const int vi = idx * (8 / M) + j;
-              sm.red[warp][s0 + k][(vi / kSN) * N + sub * kSN + vi % kSN] = v[j];
-            }
-          }
-        }
-        fold_lanes<4, L>(sp, sub);
-        fold_lanes<4, L>(s1, sub);
-        fold_lanes<4, L>(s2, sub);
-        constexpr int ML = L < 4 ? L : 4;
-        if (sub < ML) {
-#pragma unroll
-          for (int k = 0; k < 4 / ML; ++k) {
-            const int tk = s0 + grp + sub * (4 / ML) + k;
-            sm.sum[0][tk][ch] = sp[k];
-            sm.sum[1][tk][ch] = s1[k];
-            sm.sum[2][tk][ch] = s2[k];
+          for (int q = 0; q < 2; ++q) {
+            e[k][j][q] = ex2_2(mul2(dup2(d.x), a2[j][q]));
+            hh[k + 1][j][q] = fma2(e[k][j][q], hh[k][j][q], mul2(dup2(d.y), bv[q]));
           }
         }
       }
+      float sp[kSub], s1[kSub], s2[kSub];
 #pragma unroll
-      for (int i = 0; i < kSN; ++i) h[i] = h0[i];
+      for (int k = kSub - 1; k >= 0; --k) {
+        float2 bv[2], cv[2], vc[2], vb[2];  // vc, vb: this thread's part of gC and gB
+        load_pairs<2>(&sm.bc[0][k0 + k][ord][sub * kSN], bv);
+        load_pairs<2>(&sm.bc[1][k0 + k][ord][sub * kSN], cv);
+        float tp[2], t1s[2], t2[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float4 d = sm.dxg[k0 + k][col[j]];
+          const float2 dl = dup2(d.x), dx = dup2(d.y), g = dup2(d.z);
+          float2 ap, a1, aq;
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const float2 ht = hh[k + 1][j][q];
+            gh[j][q] = fma2(cv[q], g, gh[j][q]);
+            ap = q == 0 ? mul2(cv[q], ht) : fma2(cv[q], ht, ap);
+            a1 = q == 0 ? mul2(gh[j][q], bv[q]) : fma2(gh[j][q], bv[q], a1);
+            vc[q] = j == 0 ? mul2(g, ht) : fma2(g, ht, vc[q]);
+            vb[q] = j == 0 ? mul2(dx, gh[j][q]) : fma2(dx, gh[j][q], vb[q]);
+            gh[j][q] = mul2(gh[j][q], e[k][j][q]);
+            const float2 qq = mul2(gh[j][q], hh[k][j][q]);
+            aq = q == 0 ? mul2(qq, a2[j][q]) : fma2(qq, a2[j][q], aq);
+            ga[j][q] = fma2(qq, dl, ga[j][q]);
+          }
+          tp[j] = ap.x + ap.y, t1s[j] = a1.x + a1.y, t2[j] = aq.x + aq.y;
+        }
+        // over a pair's states: keep the first channel held, give the other
+        sp[k] = tp[0] + __shfl_xor_sync(0xffffffffu, tp[1], L / 2);
+        s1[k] = t1s[0] + __shfl_xor_sync(0xffffffffu, t1s[1], L / 2);
+        s2[k] = t2[0] + __shfl_xor_sync(0xffffffffu, t2[1], L / 2);
+        // over the warp's channels
+        constexpr int B1 = CP >= 4 ? 2 * L : L;  // the lane bit behind ord's 2
+        vc[0].x += __shfl_xor_sync(0xffffffffu, vc[1].x, B1);
+        vc[0].y += __shfl_xor_sync(0xffffffffu, vc[1].y, B1);
+        vb[0].x += __shfl_xor_sync(0xffffffffu, vb[1].x, B1);
+        vb[0].y += __shfl_xor_sync(0xffffffffu, vb[1].y, B1);
+        float* red = sm.red[warp][k0 + k] + sub * kSN;
+        if constexpr (CP >= 4) {
+          vc[0].x += __shfl_xor_sync(0xffffffffu, vc[0].y, L);
+          vb[0].x += __shfl_xor_sync(0xffffffffu, vb[0].y, L);
+          if constexpr (CP >= 8) {
+            const bool up = (cl & 4) != 0;
+            float v = up ? vb[0].x : vc[0].x;
+            v += __shfl_xor_sync(0xffffffffu, up ? vc[0].x : vb[0].x, 4 * L);
+            if constexpr (CP >= 16) v += __shfl_xor_sync(0xffffffffu, v, 8 * L);
+            if (CP == 8 || cl < 8) red[(up ? N : 0) + ord] = v;
+          } else {
+            red[ord] = vc[0].x;
+            red[N + ord] = vb[0].x;
+          }
+        } else {
+          red[ord] = vc[0].x, red[ord + 1] = vc[0].y;
+          red[N + ord] = vb[0].x, red[N + ord + 1] = vb[0].y;
+        }
+      }
+      constexpr int HL = L / 2, M = HL < kSub ? HL : kSub;  // lanes that hold one channel; with different tokens
+      const int hs = sub % HL;
+      fold_lanes<kSub, HL>(sp, hs);
+      fold_lanes<kSub, HL>(s1, hs);
+      fold_lanes<kSub, HL>(s2, hs);
+      __syncwarp();  // a warp alone reads its channels' columns, and has read these tokens'
+      if (hs < M) {
+#pragma unroll
+        for (int k = 0; k < kSub / M; ++k) {
+          float4& d = sm.dxg[k0 + hs * (kSub / M) + k][col[0]];
+          const float4 v = d;
+          d = make_float4(fmaf(v.x, s1[k], dsk * v.z), fmaf(v.w, s1[k], s2[k] * kLn2), fmaf(dsk, v.w, sp[k]), 0.f);
+        }
+      }
     }
+    if (ts > t0) fetch_state(ts - kTile);
     __syncthreads();
 
     if (tact && nc > 0) {
       float ox[RUN], odt[RUN], oz[RUN];
 #pragma unroll
       for (int i = 0; i < RUN; ++i) {
-        const int cc = lq * RUN + i;
-        const float4 d = sm.dxg[lt][cc];
-        const float s1 = sm.sum[1][lt][cc], s2 = sm.sum[2][lt][cc];
-        ox[i] = fmaf(d.x, s1, dsk[i] * d.z);
-        odt[i] = sig[i] * fmaf(x[i], s1, s2 * kLn2);
+        const float4 d = sm.dxg[lt][S::col(lq * RUN + i)];
+        const float2 sg = sm.sg[i][tid];
+        ox[i] = d.x;
+        odt[i] = sg.x * d.y;
         if (i < nc) gbias[i] += odt[i];
-        oz[i] = gpre[i] * fmaf(dsk[i], x[i], sm.sum[0][lt][cc]);
+        oz[i] = sg.y * d.z;
       }
       const size_t off = ((size_t)bb * f.T + ts + lt) * f.C + c0;
       store_part<T, RUN>(static_cast<T*>(p.gx) + off, nc, f.vec, ox);
@@ -249,6 +406,7 @@ __global__ void __launch_bounds__(kThreads) scan_bwd_kernel(const __grid_constan
       if (p.gz != nullptr) store_part<T, RUN>(static_cast<T*>(p.gz) + off, nc, f.vec, oz);
     }
     float* part = p.part_bc + (((size_t)ct * f.B + bb) * f.T + ts) * (2 * N);
+#pragma unroll
     for (int i = tid; i < kTile * 2 * N; i += kThreads) {
       const int tk = i / (2 * N), n = i % (2 * N);
       float s = 0.f;
@@ -256,17 +414,23 @@ __global__ void __launch_bounds__(kThreads) scan_bwd_kernel(const __grid_constan
       for (int w = 0; w < kWarps; ++w) s += sm.red[w][tk][n];
       if (ts + tk < t1) part[i] = s;
     }
-    __syncthreads();  // the next tile overwrites Δ and g, which the outputs read
+    // no barrier: the next tile's stores before its own barrier go only where this thread alone
+    // still reads (its run's columns of dxg, sg, its stages) or nobody does (bc)
   }
 
   const size_t prow = (size_t)bb * f.nseg + seg;
-  if (cact) {
-    store_vec<float, kSN>(p.part_a + (prow * f.C + c) * N + sub * kSN, ga);
-    if (seg == 0 && p.gh_in != nullptr) store_vec<float, kSN>(p.gh_in + hoff, gh);
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    if (!cact[j]) continue;
+    xor_order(ga[j], ord);
+    xor_order(gh[j], ord);
+    store_pairs<2>(p.part_a + (prow * f.C + ct * CH + ch[j]) * N + sub * kSN, ga[j]);
+    if (seg == 0 && p.gh_in != nullptr) store_pairs<2>(p.gh_in + hoff[j], gh[j]);
   }
   // gd and gdt_bias: the 16 tokens of a run of channels meet in shared memory
-  float* s_gd = &sm.sum[0][0][0];  // [16][CH] each, within sum[0] and sum[1]
-  float* s_gb = &sm.sum[1][0][0];
+  __syncthreads();
+  float* s_gd = reinterpret_cast<float*>(sm.dxg);  // [16][CH] each
+  float* s_gb = s_gd + kTile * CH;
 #pragma unroll
   for (int i = 0; i < RUN; ++i) {
     s_gd[lt * CH + lq * RUN + i] = gd[i];
@@ -282,79 +446,6 @@ __global__ void __launch_bounds__(kThreads) scan_bwd_kernel(const __grid_constan
     }
     p.part_v[(prow * 2 + 0) * f.C + ct * CH + tid] = a;
     p.part_v[(prow * 2 + 1) * f.C + ct * CH + tid] = b;
-  }
-}
-
-// The gradient that leaves segments 1 .. nseg-1 at their start, from zero at their end (the last
-// from gh_out), and their ΣΔ.  Thread = 4 states of one channel; a tile of 16 tokens through
-// shared memory.
-template <typename T, int N>
-__global__ void __launch_bounds__(kThreads) scan_bwd_summary_kernel(const __grid_constant__ ScanBwdParams p) {
-  using S = Shape<N>;
-  constexpr int L = S::kLanes, CH = S::kCh, RUN = S::kRun, TT = S::kTokThreads;
-  __shared__ float2 dg[kTile][CH];  // (Δ, g)
-  __shared__ __align__(16) float sc[kTile][N];
-  const ScanParams& f = p.f;
-  const int tid = threadIdx.x;
-  const int ct = (int)(blockIdx.x % (unsigned)f.ctiles);
-  const unsigned rest = blockIdx.x / (unsigned)f.ctiles;
-  const int seg = 1 + (int)(rest % (unsigned)(f.nseg - 1)), bb = (int)(rest / (unsigned)(f.nseg - 1));
-  const int t0 = seg * f.seg_len, t1 = min(f.T, t0 + f.seg_len);
-  const int ch = tid / L, sub = tid % L;
-  const int c = ct * CH + ch;
-  const bool cact = c < f.C;
-  const size_t hoff = ((size_t)bb * f.C + c) * N + sub * kSN;
-  float a2[kSN], gh[kSN];
-#pragma unroll
-  for (int i = 0; i < kSN; ++i) a2[i] = gh[i] = 0.f;
-  if (cact) {
-    load_rates<kSN>(f.a_log + (size_t)c * N + sub * kSN, a2);
-    if (seg == f.nseg - 1 && p.gh_out != nullptr) {
-      load_vec<float, kSN>(p.gh_out + hoff, gh);
-      store_vec<float, kSN>(p.seg_g0 + hoff, gh);
-    }
-  }
-  const int lt = tid / TT, lq = tid % TT;
-  const int c0 = ct * CH + lq * RUN, nc = max(0, min(RUN, f.C - c0));
-  float bias[RUN];
-#pragma unroll
-  for (int i = 0; i < RUN; ++i) bias[i] = f.dt_bias != nullptr && i < nc ? f.dt_bias[c0 + i] : 0.f;
-  float sumdt = 0.f;
-  for (int ts = t0 + (t1 - t0 - 1) / kTile * kTile; ts >= t0; ts -= kTile) {
-    const bool ok = ts + lt < t1;
-    const size_t row = (size_t)bb * f.T + (ok ? ts + lt : 0);
-    const int n = ok ? nc : 0;
-    float dt[RUN], g[RUN], z[RUN];
-    load_part<T, RUN>(static_cast<const T*>(f.dt) + row * f.lddt + c0, n, f.vec, dt);
-    load_part<T, RUN>(static_cast<const T*>(p.gy) + row * f.C + c0, n, f.vec, g);
-    if (f.z != nullptr) load_part<T, RUN>(static_cast<const T*>(f.z) + row * f.ldz + c0, n, f.vec, z);
-#pragma unroll
-    for (int i = 0; i < RUN; ++i) {
-      float sig;
-      const float delta = softplus(dt[i] + bias[i], sig);
-      if (f.z != nullptr) g[i] *= z[i] * sigmoid(z[i]);
-      dg[lt][lq * RUN + i] = i < n ? make_float2(delta, g[i]) : make_float2(0.f, 0.f);
-    }
-    for (int i = tid; i < kTile * N; i += kThreads) {
-      const int tk = i / N;
-      sc[tk][i % N] = ts + tk < t1 ? IO<T>::to_f(static_cast<const T*>(f.c)[((size_t)bb * f.T + ts + tk) * f.ldc + i % N])
-                                   : 0.f;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int k = kTile - 1; k >= 0; --k) {
-      const float2 d = dg[k][ch];
-      float cv[kSN];
-      load_vec<float, kSN>(&sc[k][sub * kSN], cv);
-#pragma unroll
-      for (int i = 0; i < kSN; ++i) gh[i] = ex2(d.x * a2[i]) * fmaf(cv[i], d.y, gh[i]);
-      sumdt += d.x;
-    }
-    __syncthreads();
-  }
-  if (cact) {
-    store_vec<float, kSN>(p.seg_g + (size_t)seg * f.B * f.C * N + hoff, gh);
-    if (sub == 0) p.seg_dt[((size_t)seg * f.B + bb) * f.C + c] = sumdt;
   }
 }
 
@@ -395,14 +486,22 @@ template <typename T, int N>
 cudaError_t bwd_n(ScanBwdParams p, cudaStream_t st) {
   static unsigned mask = 0;
   p.f.ctiles = (p.f.C + Shape<N>::kCh - 1) / Shape<N>::kCh;
-  const unsigned rows = (unsigned)p.f.ctiles * (unsigned)p.f.B;
-  cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(scan_bwd_kernel<T, N>), (int)sizeof(Smem<N>), &mask);
+  constexpr int kSmem = (int)sizeof(Smem<T, N>);
+  cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(scan_bwd_kernel<T, N>), kSmem, &mask);
   if (e != cudaSuccess) return e;
   if (p.f.nseg > 1) {
-    scan_bwd_summary_kernel<T, N><<<rows * (unsigned)(p.f.nseg - 1), kThreads, 0, st>>>(p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    ScanParams r = p.f;
+    r.x = p.gy;
+    r.ldx = p.f.C;
+    r.b = p.f.c;
+    r.ldb = p.f.ldc;
+    r.h_in = p.gh_out;
+    r.seg_h = p.seg_g;
+    r.seg_dt = p.seg_dt;
+    r.seg_h0 = p.seg_g0;
+    if ((e = launch_scan_reverse(sizeof(T) == 2, r, st)) != cudaSuccess) return e;
   }
-  scan_bwd_kernel<T, N><<<rows * (unsigned)p.f.nseg, kThreads, sizeof(Smem<N>), st>>>(p);
+  scan_bwd_kernel<T, N><<<(unsigned)p.f.ctiles * (unsigned)p.f.B * (unsigned)p.f.nseg, kThreads, kSmem, st>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const size_t n = (size_t)p.f.B * p.f.T * 2 * N;
   scan_bwd_bc_kernel<T><<<(unsigned)((n + 255) / 256), 256, 0, st>>>(p.f.ctiles, n, N, p.part_bc,
@@ -427,7 +526,7 @@ cudaError_t bwd_t(const ScanBwdParams& p, cudaStream_t st) {
 
 }  // namespace
 
-int scan_bwd_channels(int N) { return kThreads * kSN / N; }
+int scan_bwd_channels(int N) { return 2 * kThreads * kSN / N; }
 
 cudaError_t launch_scan_bwd(bool bf16, const ScanBwdParams& p, cudaStream_t st) {
   return bf16 ? bwd_t<__nv_bfloat16>(p, st) : bwd_t<float>(p, st);

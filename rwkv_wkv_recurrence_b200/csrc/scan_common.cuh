@@ -5,6 +5,53 @@
 
 namespace rwkv {
 
+// Two fp32 operations in one instruction (sm_100 packed arithmetic); each half rounds as the single
+// instruction does.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<unsigned long long&>(d))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)),
+        "l"(reinterpret_cast<unsigned long long&>(c)));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<unsigned long long&>(d))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<unsigned long long&>(d))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+  return d;
+}
+__device__ __forceinline__ float2 dup2(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 ex2_2(float2 x) { return make_float2(ex2(x.x), ex2(x.y)); }
+
+// softplus(v) = log(1 + e^v) = max(v, 0) + log1p(e^-|v|) of two values.  log1p(e) = e P(e) on
+// [0, 1], P the polynomial of degree 9 through log1p(e)/e at the Chebyshev points: within 2.1 half
+// steps in fp32 arithmetic over all e (so that small steps, e^v far below 1, keep their relative
+// accuracy), without a division.  e01 receives e^-|v|.  NaN and the infinities pass through.
+__device__ __forceinline__ float2 softplus2(float2 v, float2& e01) {
+  const float2 a = make_float2(-fabsf(v.x), -fabsf(v.y));
+  const float2 e = ex2_2(fma2(a, dup2(kL2eLo), mul2(a, dup2(kL2eHi))));
+  e01 = e;
+  float2 r = fma2(e, dup2(-0.0031760570127516985f), dup2(0.019542526453733444f));
+  r = fma2(r, e, dup2(-0.056373611092567444f));
+  r = fma2(r, e, dup2(0.10543623566627502f));
+  r = fma2(r, e, dup2(-0.1526966691017151f));
+  r = fma2(r, e, dup2(0.1966327428817749f));
+  r = fma2(r, e, dup2(-0.24951615929603577f));
+  r = fma2(r, e, dup2(0.33329710364341736f));
+  r = fma2(r, e, dup2(-0.49999892711639404f));
+  r = fma2(r, e, dup2(1.0f));
+  return fma2(r, e, make_float2(fmaxf(v.x, 0.f), fmaxf(v.y, 0.f)));
+}
+
 // A log2(e) = -exp(a_log) log2(e) of n states, so that exp(Δ A) = 2^(Δ a2).  A rate beyond the
 // largest float counts as that one, which keeps 0 · a2 = 0 at the positions past a segment's end.
 template <int K>
@@ -13,6 +60,30 @@ __device__ __forceinline__ void load_rates(const float* __restrict__ a_log, floa
   for (int i = 0; i < K; ++i) {
     const float r = -expf(a_log[i]) * kL2eHi;
     a2[i] = r < -3.402823466e+38f ? -3.402823466e+38f : r;  // a NaN stays
+  }
+}
+
+// 2 P consecutive floats as pairs (P = 1: 8-byte, else 16-byte accesses).
+template <int P>
+__device__ __forceinline__ void load_pairs(const float* p, float2 (&v)[P]) {
+  if constexpr (P == 1) {
+    v[0] = *reinterpret_cast<const float2*>(p);
+  } else {
+#pragma unroll
+    for (int i = 0; i < P; i += 2) {
+      const float4 x = *reinterpret_cast<const float4*>(p + 2 * i);
+      v[i] = make_float2(x.x, x.y), v[i + 1] = make_float2(x.z, x.w);
+    }
+  }
+}
+template <int P>
+__device__ __forceinline__ void store_pairs(float* p, const float2 (&v)[P]) {
+  if constexpr (P == 1) {
+    *reinterpret_cast<float2*>(p) = v[0];
+  } else {
+#pragma unroll
+    for (int i = 0; i < P; i += 2)
+      *reinterpret_cast<float4*>(p + 2 * i) = make_float4(v[i].x, v[i].y, v[i + 1].x, v[i + 1].y);
   }
 }
 

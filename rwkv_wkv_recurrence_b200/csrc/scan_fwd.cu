@@ -9,14 +9,16 @@
 // 8 bytes in bf16 but needs 16 ex2, and the special-function unit does 16 a clock and SM, so the
 // exponentials take about three times as long as the bytes.
 //
-// Mapping.  A thread owns 4 states of one channel, N/4 neighbouring lanes a channel; a CTA of 128
-// threads owns 512/N channels of one batch row over one time segment, 32 tokens at a time:
-//   1. the inputs of a tile are read in runs of 128/N channels per thread (16 bytes in bf16 with
-//      N = 16), a tile ahead in registers; Δ and Δx go to shared memory, so softplus is done once
-//      per element and not once per lane, and B, C as fp32 rows;
-//   2. each thread walks the 32 tokens; Σ_n over a channel's lanes is folded four tokens at a time
-//      (three shuffles for four sums instead of eight), the sums go to shared memory;
-//   3. the tile's outputs get d x and the gate and leave in the same runs.
+// Mapping.  A thread owns 4 states of one channel, the lanes of a warp are channels; a CTA owns 16
+// or 32 channels of one batch row over one time segment, 32 tokens at a time:
+//   1. the inputs of a tile are read in runs of channels per thread (16 bytes in bf16 with N = 16),
+//      a tile ahead, left as loaded in registers until the tile is due; Δ and Δx go to shared
+//      memory, so softplus is done once per element and not once per group of states, and B, C as
+//      fp32 rows;
+//   2. each thread walks the 32 tokens, reading 4 of them ahead; Σ_n over its 4 states goes to
+//      shared memory per group of states (folding a channel's states over lanes instead costs
+//      three shuffles and nine selects and adds per 4 tokens, and measured 0.473 ms);
+//   3. the tile's outputs add the groups' sums, d x and the gate and leave in the same runs.
 //
 // Few channels, long axis: time is cut into segments.  A first launch runs every segment but the
 // last from a zero state and keeps the state it reaches and ΣΔ; the state entering segment s is
@@ -31,149 +33,206 @@
 namespace rwkv {
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kTile = 32;  // tokens per tile
-constexpr int kSN = 4;     // states per thread
+constexpr int kSN = 4;  // states per thread
 
-template <int N>
+// kOutputs writes outputs; kSummary the states and ΣΔ at the segments' ends, from zero; kReverse
+// the same for the backward's recurrence G <- exp(Δ_t A) (G + C_t g_t) over reversed time, with
+// g = gy silu(z): gy in the place of x, C of B, gh_out of h_in.
+enum class Pass { kSummary, kOutputs, kReverse };
+
+// Channels per CTA: small CTAs (two warps with N = 16) spread evenly over the SMs; 32 channels
+// measured the same there (0.390 against 0.383 ms at 4x4096x2560).
+constexpr int scan_channels(int N) { return N == 8 ? 32 : 16; }
+
+// CH channels per CTA; thread tid owns states 4 (tid / CH) .. + 3 of channel tid mod CH.
+template <int N, int CH_>
 struct Shape {
-  static constexpr int kLanes = N / kSN;                // lanes per channel
-  static constexpr int kCh = kThreads / kLanes;         // channels per CTA
-  static constexpr int kRun = kCh / (kThreads / kTile); // channels per thread in the tile's loads
-  static constexpr int kSt = N / (kThreads / kTile);    // states per thread in the tile's loads
+  static constexpr int kCh = CH_;
+  static constexpr int kGroups = N / kSN;                   // threads per channel
+  static constexpr int kThreads = kCh * kGroups;
+  static constexpr int kTile = 32;                          // tokens per tile
+  static constexpr int kTokThreads = kThreads / kTile;      // threads per token in the tile's loads
+  static constexpr int kRun = kCh / kTokThreads;            // channels per thread there
+  static constexpr int kQuads = kTile * N / 4 / kThreads;   // groups of 4 states of B (and C) per thread there
+  static_assert(kTokThreads * kRun == kCh && kQuads * kThreads * 4 == kTile * N, "a tile's loads cover it");
+  static_assert(kRun % 2 == 0, "channels are worked on in pairs");
 };
 
-template <int N>
+// 4 states' B and C of one token.  As fp32: kept in bf16 they would load in half the turns of the
+// shared-memory pipe, but unpacking them costs more issue slots than that saves (4x4096x2560 bf16:
+// 0.422 against 0.383 ms).
+struct __align__(16) BC4 {
+  float b[4], c[4];
+};
+
+// Rows of dx are padded so that the tile's stores (a run of channels per thread) fall on different
+// banks, the groups' sums so that two groups in one warp do.
+template <int N, typename S>
 struct __align__(16) Smem {
-  float2 dx[kTile][Shape<N>::kCh];      // (Δ, Δ x)
-  float b[kTile][N], c[kTile][N];
-  float y[kTile][Shape<N>::kCh + 8];    // Σ_n C h; rows 8 words apart from a multiple of 32 banks
+  float2 dx[S::kTile][S::kCh + 2];                          // (Δ, Δ x)
+  BC4 bc[S::kTile][S::kGroups];
+  float y[S::kGroups][S::kTile * S::kCh + (S::kCh & 31)];   // Σ C h over each group of 4 states
 };
 
 // One tile's inputs in registers, as loaded.
-template <typename T, int N>
+template <typename T, typename S>
 struct Tile {
-  float x[Shape<N>::kRun], dt[Shape<N>::kRun], z[Shape<N>::kRun], b[Shape<N>::kSt], c[Shape<N>::kSt];
+  Raw<T, S::kRun> x, dt, z;
+  Raw<T, 4> b[S::kQuads], c[S::kQuads];
 };
 
-template <typename T, int N, bool OUT>
-__device__ __forceinline__ void load_tile(Tile<T, N>& R, const ScanParams& p, int bb, int t, int t1, int c0, int nc,
-                                          int s0) {
-  constexpr int RUN = Shape<N>::kRun, ST = Shape<N>::kSt;
+// The tile at token ts: this thread's token is t, its channels c0 .. c0 + nc - 1.
+template <typename T, int N, typename S, Pass PASS>
+__device__ __forceinline__ void load_tile(Tile<T, S>& R, const ScanParams& p, int bb, int ts, int t, int t1, int c0,
+                                          int nc) {
   const bool ok = t < t1;
   const size_t row = (size_t)bb * p.T + (ok ? t : 0);
   const int n = ok ? nc : 0;
-  load_part<T, RUN>(static_cast<const T*>(p.x) + row * p.ldx + c0, n, p.vec, R.x);
-  load_part<T, RUN>(static_cast<const T*>(p.dt) + row * p.lddt + c0, n, p.vec, R.dt);
-  load_part<T, ST>(static_cast<const T*>(p.b) + row * p.ldb + s0, ok ? ST : 0, p.vec_bc, R.b);
-  if constexpr (OUT) {
-    if (p.z != nullptr) load_part<T, RUN>(static_cast<const T*>(p.z) + row * p.ldz + c0, n, p.vec, R.z);
-    load_part<T, ST>(static_cast<const T*>(p.c) + row * p.ldc + s0, ok ? ST : 0, p.vec_bc, R.c);
+  R.x.load(static_cast<const T*>(p.x) + row * p.ldx + c0, n, p.vec);
+  R.dt.load(static_cast<const T*>(p.dt) + row * p.lddt + c0, n, p.vec);
+  if constexpr (PASS != Pass::kSummary)
+    if (p.z != nullptr) R.z.load(static_cast<const T*>(p.z) + row * p.ldz + c0, n, p.vec);
+#pragma unroll
+  for (int k = 0; k < S::kQuads; ++k) {
+    const int id = threadIdx.x + k * S::kThreads, tq = ts + id / (N / 4), s0 = id % (N / 4) * 4;
+    const bool on = tq < t1;
+    const size_t rq = (size_t)bb * p.T + (on ? tq : 0);
+    R.b[k].load(static_cast<const T*>(p.b) + rq * p.ldb + s0, on ? 4 : 0, p.vec_bc);
+    if constexpr (PASS == Pass::kOutputs) R.c[k].load(static_cast<const T*>(p.c) + rq * p.ldc + s0, on ? 4 : 0, p.vec_bc);
   }
 }
 
-// OUT: the pass that writes outputs; else the summary pass (states and ΣΔ at the segments' ends).
-template <typename T, int N, bool OUT>
-__global__ void __launch_bounds__(kThreads) scan_fwd_kernel(const __grid_constant__ ScanParams p) {
-  using S = Shape<N>;
-  constexpr int L = S::kLanes, CH = S::kCh, RUN = S::kRun, ST = S::kSt;
-  __shared__ Smem<N> sm;
+// What the scan reads of 4 tokens from shared memory.
+struct Quad {
+  float2 dx[4], b[4][2], c[4][2];
+  template <typename SM, bool OUT>
+  __device__ __forceinline__ void load(const SM& sm, int tk, int ch, int g) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      dx[k] = sm.dx[tk + k][ch];
+      load_pairs<2>(sm.bc[tk + k][g].b, b[k]);
+      if constexpr (OUT) load_pairs<2>(sm.bc[tk + k][g].c, c[k]);
+    }
+  }
+};
+
+template <typename T, int N, int CH_, Pass PASS>
+__global__ void __launch_bounds__(Shape<N, CH_>::kThreads) scan_fwd_kernel(const __grid_constant__ ScanParams p) {
+  using S = Shape<N, CH_>;
+  using SM = Smem<N, S>;
+  constexpr int CH = S::kCh, RUN = S::kRun, TT = S::kTokThreads, TL = S::kTile;
+  constexpr bool OUT = PASS == Pass::kOutputs, REV = PASS == Pass::kReverse;
+  extern __shared__ __align__(16) unsigned char raw[];
+  SM& sm = *reinterpret_cast<SM*>(raw);
   const int tid = threadIdx.x;
   const int ct = (int)(blockIdx.x % (unsigned)p.ctiles);
   const unsigned rest = blockIdx.x / (unsigned)p.ctiles;
-  const int nseg = OUT ? p.nseg : p.nseg - 1;  // the last segment's summary is not needed
-  const int seg = (int)(rest % (unsigned)nseg), bb = (int)(rest / (unsigned)nseg);
+  const int nseg = OUT ? p.nseg : p.nseg - 1;
+  // the last segment in the pass's own time has no segment behind it that would need its summary
+  const int seg = (int)(rest % (unsigned)nseg) + (REV ? 1 : 0), bb = (int)(rest / (unsigned)nseg);
   const int t0 = seg * p.seg_len, t1 = min(p.T, t0 + p.seg_len);
 
-  // the scan's view: 4 states of one channel
-  const int ch = tid / L, sub = tid % L;
-  const int c = ct * CH + ch;
-  const bool cact = c < p.C;
-  const size_t hoff = ((size_t)bb * p.C + c) * N + sub * kSN;  // in a [B,C,N] state
-  const size_t plane = (size_t)p.B * p.C * N;
-  float a2[kSN], h[kSN];
-#pragma unroll
-  for (int i = 0; i < kSN; ++i) a2[i] = h[i] = 0.f;
-  if (cact) {
-    load_rates<kSN>(p.a_log + (size_t)c * N + sub * kSN, a2);
-    if (OUT && seg > 0) {
-      load_vec<float, kSN>(p.seg_h + hoff, h);  // segment 0's summary starts from h_in
-      for (int s = 1; s < seg; ++s) {
-        float x[kSN];
-        load_vec<float, kSN>(p.seg_h + (size_t)s * plane + hoff, x);
-        const float sd = p.seg_dt[((size_t)s * p.B + bb) * p.C + c];
-#pragma unroll
-        for (int i = 0; i < kSN; ++i) h[i] = fmaf(ex2(sd * a2[i]), h[i], x[i]);
-      }
-    } else if (seg == 0) {
-      // with segments the first launch keeps a copy of h_in, which the second reads: h_out may be
-      // the same array, and another CTA of the second launch writes it
-      const float* hi = OUT && p.nseg > 1 ? p.seg_h0 : p.h_in;
-      if (p.h_in != nullptr) load_vec<float, kSN>(hi + hoff, h);
-      if (!OUT && p.h_in != nullptr) store_vec<float, kSN>(p.seg_h0 + hoff, h);
-    }
-  }
-
   // the loads' view: one token of the tile, a run of channels, a run of states
-  const int lt = tid / (kThreads / kTile), lq = tid % (kThreads / kTile);
+  const int lt = tid / TT, lq = tid % TT;
   const int c0 = ct * CH + lq * RUN, nc = max(0, min(RUN, p.C - c0));
+  Tile<T, S> R;
+  const int first = REV ? t0 + (t1 - t0 - 1) / TL * TL : t0;  // the first tile worked on
+  load_tile<T, N, S, PASS>(R, p, bb, first, first + lt, t1, c0, nc);
   float bias[RUN], dsk[RUN];
 #pragma unroll
   for (int i = 0; i < RUN; ++i) {
     bias[i] = p.dt_bias != nullptr && i < nc ? p.dt_bias[c0 + i] : 0.f;
     dsk[i] = OUT && p.d != nullptr && i < nc ? p.d[c0 + i] : 0.f;
   }
-  Tile<T, N> R;
-  load_tile<T, N, OUT>(R, p, bb, t0 + lt, t1, c0, nc, lq * ST);
+
+  // the scan's view: 4 states of one channel, in pairs
+  const int ch = tid % CH, s0 = tid / CH * kSN;
+  const int c = ct * CH + ch;
+  const bool cact = c < p.C;
+  const size_t hoff = ((size_t)bb * p.C + c) * N + s0;  // in a [B,C,N] state
+  const size_t plane = (size_t)p.B * p.C * N;
+  float a2f[kSN] = {0.f, 0.f, 0.f, 0.f};
+  if (cact) load_rates<kSN>(p.a_log + (size_t)c * N + s0, a2f);
+  float2 a2[2] = {make_float2(a2f[0], a2f[1]), make_float2(a2f[2], a2f[3])}, h[2] = {dup2(0.f), dup2(0.f)};
+  if (cact) {
+    if (OUT && seg > 0) {
+      load_pairs<2>(p.seg_h + hoff, h);  // segment 0's summary starts from h_in
+      for (int s = 1; s < seg; ++s) {
+        float2 x[2];
+        load_pairs<2>(p.seg_h + (size_t)s * plane + hoff, x);
+        const float2 sd = dup2(p.seg_dt[((size_t)s * p.B + bb) * p.C + c]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) h[i] = fma2(ex2_2(mul2(sd, a2[i])), h[i], x[i]);
+      }
+    } else if (seg == (REV ? p.nseg - 1 : 0) && p.h_in != nullptr) {
+      // with segments the first launch keeps a copy of h_in, which the second reads: h_out may be
+      // the same array, and another CTA of the second launch writes it
+      load_pairs<2>((OUT && p.nseg > 1 ? p.seg_h0 : p.h_in) + hoff, h);
+      if (!OUT) store_pairs<2>(p.seg_h0 + hoff, h);
+    }
+  }
   float sumdt = 0.f;
 
-  for (int ts = t0; ts < t1; ts += kTile) {
+  for (int ts = first; ts >= t0 && ts < t1; ts += REV ? -TL : TL) {
     const bool tact = ts + lt < t1;
     float x[RUN], z[RUN];
 #pragma unroll
-    for (int i = 0; i < RUN; ++i) {
-      float sig, delta = softplus(R.dt[i] + bias[i], sig);
-      if (!tact || i >= nc) delta = 0.f;
-      x[i] = R.x[i];
-      if constexpr (OUT) z[i] = R.z[i];
-      sm.dx[lt][lq * RUN + i] = make_float2(delta, tact && i < nc ? delta * x[i] : 0.f);
+    for (int i = 0; i < RUN; i += 2) {
+      float2 e;
+      const float2 dl = softplus2(make_float2(R.dt[i] + bias[i], R.dt[i + 1] + bias[i + 1]), e);
+      x[i] = R.x[i], x[i + 1] = R.x[i + 1];
+      if constexpr (OUT) z[i] = R.z[i], z[i + 1] = R.z[i + 1];
+      float2 in = make_float2(dl.x * x[i], dl.y * x[i + 1]);
+      if constexpr (REV) {
+        in = make_float2(x[i], x[i + 1]);
+        if (p.z != nullptr) in = make_float2(x[i] * (R.z[i] * sigmoid(R.z[i])), x[i + 1] * (R.z[i + 1] * sigmoid(R.z[i + 1])));
+      }
+      const bool on0 = tact && i < nc, on1 = tact && i + 1 < nc;
+      *reinterpret_cast<float4*>(&sm.dx[lt][lq * RUN + i]) =
+          make_float4(on0 ? dl.x : 0.f, on0 ? in.x : 0.f, on1 ? dl.y : 0.f, on1 ? in.y : 0.f);
     }
-    store_vec<float, ST>(&sm.b[lt][lq * ST], R.b);
-    if constexpr (OUT) store_vec<float, ST>(&sm.c[lt][lq * ST], R.c);
-    if (ts + kTile < t1) load_tile<T, N, OUT>(R, p, bb, ts + kTile + lt, t1, c0, nc, lq * ST);
+#pragma unroll
+    for (int k = 0; k < S::kQuads; ++k) {
+      BC4& q = (&sm.bc[0][0])[tid + k * S::kThreads];
+      *reinterpret_cast<float4*>(q.b) = make_float4(R.b[k][0], R.b[k][1], R.b[k][2], R.b[k][3]);
+      if constexpr (OUT) *reinterpret_cast<float4*>(q.c) = make_float4(R.c[k][0], R.c[k][1], R.c[k][2], R.c[k][3]);
+    }
+    const int tn = REV ? ts - TL : ts + TL;
+    if (tn >= t0 && tn < t1) load_tile<T, N, S, PASS>(R, p, bb, tn, tn + lt, t1, c0, nc);
     __syncthreads();
 
-#pragma unroll 2
-    for (int g = 0; g < kTile; g += 4) {
+#pragma unroll 1
+    for (int hh = 0; hh < TL; hh += kScanCkLen) {
+      const int hf = REV ? TL - kScanCkLen - hh : hh;
+      if (ts + hf >= t1) continue;
       if constexpr (OUT) {
-        if (p.ckpt != nullptr && g % kScanCkLen == 0 && cact && ts + g < t1)
-          store_vec<float, kSN>(p.ckpt + (size_t)((ts + g) / kScanCkLen) * plane + hoff, h);
+        if (p.ckpt != nullptr && cact)
+          store_pairs<2>(p.ckpt + (size_t)((ts + hf) / kScanCkLen) * plane + hoff, h);
       }
-      float y[4];
+      Quad q;
+      q.template load<SM, OUT>(sm, hf + (REV ? kScanCkLen - 4 : 0), ch, s0 / kSN);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float2 dx = sm.dx[g + k][ch];
-        float bv[kSN], cv[kSN];
-        load_vec<float, kSN>(&sm.b[g + k][sub * kSN], bv);
+      for (int gg = 0; gg < kScanCkLen; gg += 4) {
+        const int g = REV ? kScanCkLen - 4 - gg : gg;
+        Quad nx = q;  // the next 4 tokens, on their way while these are worked on
+        if (gg + 4 < kScanCkLen) nx.template load<SM, OUT>(sm, hf + (REV ? g - 4 : g + 4), ch, s0 / kSN);
 #pragma unroll
-        for (int i = 0; i < kSN; ++i) h[i] = fmaf(ex2(dx.x * a2[i]), h[i], dx.y * bv[i]);
-        if constexpr (OUT) {
-          load_vec<float, kSN>(&sm.c[g + k][sub * kSN], cv);
-          y[k] = fmaf(cv[0], h[0], cv[1] * h[1]) + fmaf(cv[2], h[2], cv[3] * h[3]);
-        } else {
-          sumdt += dx.x;
+        for (int kk = 0; kk < 4; ++kk) {
+          const int k = REV ? 3 - kk : kk;
+          const float2 d2 = dup2(q.dx[k].x), in2 = dup2(q.dx[k].y);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float2 e = ex2_2(mul2(d2, a2[i]));
+            h[i] = REV ? mul2(e, fma2(in2, q.b[k][i], h[i])) : fma2(e, h[i], mul2(in2, q.b[k][i]));
+          }
+          if constexpr (OUT) {
+            const float2 acc = fma2(q.c[k][1], h[1], mul2(q.c[k][0], h[0]));
+            sm.y[s0 / kSN][(hf + g + k) * CH + ch] = acc.x + acc.y;
+          } else {
+            sumdt += q.dx[k].x;
+          }
         }
-      }
-      if constexpr (OUT) {
-        // y[k] of token g + k summed over the channel's L lanes: lane bits 1 and 0 pick tokens
-        if constexpr (L >= 4) {
-          fold_lanes<4, L>(y, sub);
-          if (sub < 4) sm.y[g + sub][ch] = y[0];
-        } else {
-          fold_lanes<4, L>(y, sub);
-#pragma unroll
-          for (int k = 0; k < 4 / L; ++k) sm.y[g + sub * (4 / L) + k][ch] = y[k];
-        }
+        q = nx;
       }
     }
     __syncthreads();
@@ -182,9 +241,17 @@ __global__ void __launch_bounds__(kThreads) scan_fwd_kernel(const __grid_constan
       if (p.y != nullptr && tact && nc > 0) {
         float o[RUN];
 #pragma unroll
-        for (int i = 0; i < RUN; ++i) {
-          o[i] = fmaf(dsk[i], x[i], sm.y[lt][lq * RUN + i]);
-          if (p.z != nullptr) o[i] *= z[i] * sigmoid(z[i]);
+        for (int i = 0; i < RUN; ++i) o[i] = dsk[i] * x[i];
+#pragma unroll
+        for (int g = 0; g < S::kGroups; ++g) {
+          float v[RUN];
+          load_vec<float, RUN>(&sm.y[g][lt * CH + lq * RUN], v);
+#pragma unroll
+          for (int i = 0; i < RUN; ++i) o[i] += v[i];
+        }
+        if (p.z != nullptr) {
+#pragma unroll
+          for (int i = 0; i < RUN; ++i) o[i] *= z[i] * sigmoid(z[i]);
         }
         store_part<T, RUN>(static_cast<T*>(p.y) + ((size_t)bb * p.T + ts + lt) * p.C + c0, nc, p.vec, o);
       }
@@ -193,45 +260,60 @@ __global__ void __launch_bounds__(kThreads) scan_fwd_kernel(const __grid_constan
 
   if (cact) {
     if constexpr (OUT) {
-      if (seg == p.nseg - 1 && p.h_out != nullptr) store_vec<float, kSN>(p.h_out + hoff, h);
+      if (seg == p.nseg - 1 && p.h_out != nullptr) store_pairs<2>(p.h_out + hoff, h);
     } else {
-      store_vec<float, kSN>(p.seg_h + (size_t)seg * plane + hoff, h);
-      if (sub == 0) p.seg_dt[((size_t)seg * p.B + bb) * p.C + c] = sumdt;
+      store_pairs<2>(p.seg_h + (size_t)seg * plane + hoff, h);
+      if (s0 == 0) p.seg_dt[((size_t)seg * p.B + bb) * p.C + c] = sumdt;
     }
   }
 }
 
-template <typename T, int N>
-cudaError_t fwd_n(ScanParams p, cudaStream_t st) {
-  p.ctiles = (p.C + Shape<N>::kCh - 1) / Shape<N>::kCh;
-  const unsigned rows = (unsigned)p.ctiles * (unsigned)p.B;
-  if (p.nseg > 1) {
-    scan_fwd_kernel<T, N, false><<<rows * (unsigned)(p.nseg - 1), kThreads, 0, st>>>(p);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-  }
-  scan_fwd_kernel<T, N, true><<<rows * (unsigned)p.nseg, kThreads, 0, st>>>(p);
+template <typename T, int N, int CH, Pass PASS>
+cudaError_t launch_pass(const ScanParams& p, cudaStream_t st) {
+  constexpr int kThreads = Shape<N, CH>::kThreads, kSmem = (int)sizeof(Smem<N, Shape<N, CH>>);
+  static unsigned mask = 0;
+  const auto kernel = scan_fwd_kernel<T, N, CH, PASS>;
+  const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kernel), kSmem, &mask);
+  if (e != cudaSuccess) return e;
+  const unsigned segs = (unsigned)(PASS == Pass::kOutputs ? p.nseg : p.nseg - 1);
+  kernel<<<(unsigned)p.ctiles * (unsigned)p.B * segs, kThreads, kSmem, st>>>(p);
   return cudaGetLastError();
 }
 
+template <typename T, int N>
+cudaError_t run_n(ScanParams p, bool reverse, cudaStream_t st) {
+  constexpr int CH = scan_channels(N);
+  p.ctiles = (p.C + CH - 1) / CH;
+  if (reverse) return launch_pass<T, N, CH, Pass::kReverse>(p, st);
+  if (p.nseg > 1) {
+    const cudaError_t e = launch_pass<T, N, CH, Pass::kSummary>(p, st);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_pass<T, N, CH, Pass::kOutputs>(p, st);
+}
+
 template <typename T>
-cudaError_t fwd_t(const ScanParams& p, cudaStream_t st) {
+cudaError_t run_t(const ScanParams& p, bool reverse, cudaStream_t st) {
   switch (p.N) {
-    case 8: return fwd_n<T, 8>(p, st);
-    case 16: return fwd_n<T, 16>(p, st);
-    case 32: return fwd_n<T, 32>(p, st);
-    case 64: return fwd_n<T, 64>(p, st);
+    case 8: return run_n<T, 8>(p, reverse, st);
+    case 16: return run_n<T, 16>(p, reverse, st);
+    case 32: return run_n<T, 32>(p, reverse, st);
+    case 64: return run_n<T, 64>(p, reverse, st);
   }
   return cudaErrorInvalidValue;
 }
 
 }  // namespace
 
-int scan_fwd_channels(int N) { return kThreads * kSN / N; }
-int scan_tile_tokens() { return kTile; }
+int scan_fwd_channels(int N) { return scan_channels(N); }
+int scan_tile_tokens() { return 32; }
 
 cudaError_t launch_scan_fwd(bool bf16, const ScanParams& p, cudaStream_t st) {
-  return bf16 ? fwd_t<__nv_bfloat16>(p, st) : fwd_t<float>(p, st);
+  return bf16 ? run_t<__nv_bfloat16>(p, false, st) : run_t<float>(p, false, st);
+}
+
+cudaError_t launch_scan_reverse(bool bf16, const ScanParams& p, cudaStream_t st) {
+  return bf16 ? run_t<__nv_bfloat16>(p, true, st) : run_t<float>(p, true, st);
 }
 
 }  // namespace rwkv
