@@ -9,10 +9,11 @@
 //   gw[c][j] = Σ_{b,t} g_t x_{t-W+1+j},   gbias[c] = Σ_{b,t} g_t.
 // pre is recomputed from x (W FMAs) rather than kept by the forward.
 //
-// Everything is one pass over the data, so bandwidth bounds it.  A thread owns V channels (one
-// 16-byte access, 8-byte in the bf16 backward, whose two windows and W+1 sums would not fit in
-// registers at 8 channels) of one stretch of tokens and slides a W-token window along it in
-// registers; neighbouring stretches re-read W-1 tokens, which come from L2.
+// Everything is one pass over the data, so bandwidth bounds it.  A thread owns V channels of one
+// stretch of tokens and slides a W-token window along it in registers; the tokens ahead are fetched
+// 8 at a time and left as loaded until they are due.  V is small (8 bytes a load forward, 4 to 8
+// backward, whose two windows and W+1 sums are kept besides) so that enough threads fit on an SM to
+// keep its loads in flight.  Neighbouring stretches re-read W-1 tokens, which come from L2.
 #include "launch.h"
 #include "mixer_common.cuh"
 
@@ -23,7 +24,7 @@ constexpr int kThreads = 128;
 constexpr int kFwdStretch = 32;  // tokens per thread, forward
 constexpr int kBwdStretch = 64;  // tokens per thread, backward
 constexpr int kBwdWarps = 8;     // stretches per CTA (their weight-gradient sums meet in shared memory)
-constexpr int kAhead = 4;        // tokens loaded together
+constexpr int kAhead = 8;        // tokens fetched together
 
 // Element of the concatenation (state, x): position k < W-1 is state row k, the rest token k-(W-1).
 template <typename T, int V, int W>
@@ -61,11 +62,18 @@ __global__ void __launch_bounds__(kThreads) conv_fwd_kernel(ConvParams p) {
   for (int j = 0; j < W - 1; ++j) load_pos<T, V, W>(p, b, t0 + j, c, win[j + 1]);
   const T* xr = static_cast<const T*>(p.x) + (size_t)b * p.T * p.ldx + c;
   T* yr = static_cast<T*>(p.y) + (size_t)b * p.T * p.C + c;
-  for (int t = t0; t < t1; t += kAhead) {
-    float nx[kAhead][V];
+  Raw<T, V> nx[kAhead];
+  const auto fetch = [&](int t) {
 #pragma unroll
     for (int a = 0; a < kAhead; ++a)
-      if (t + a < t1) load_vec<T, V>(xr + (size_t)(t + a) * p.ldx, nx[a]);
+      if (t + a < t1) nx[a].load(xr + (size_t)(t + a) * p.ldx, V, true);
+  };
+  fetch(t0);
+  for (int t = t0; t < t1; t += kAhead) {
+    Raw<T, V> cur[kAhead];
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) cur[a] = nx[a];
+    fetch(t + kAhead);
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) {
       if (t + a >= t1) break;
@@ -74,11 +82,11 @@ __global__ void __launch_bounds__(kThreads) conv_fwd_kernel(ConvParams p) {
       for (int i = 0; i < V; ++i) {
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) win[j][i] = win[j + 1][i];
-        win[W - 1][i] = nx[a][i];
+        win[W - 1][i] = cur[a][i];
         float acc = bias[i];
 #pragma unroll
         for (int j = 0; j < W; ++j) acc = fmaf(w[j][i], win[j][i], acc);
-        o[i] = p.silu ? acc * sigmoid(acc) : acc;
+        o[i] = p.silu ? acc * sigmoid_ex2(acc) : acc;
       }
       store_vec<T, V>(yr + (size_t)(t + a) * p.C, o);
     }
@@ -131,14 +139,21 @@ __global__ void __launch_bounds__(32 * kBwdWarps) conv_bwd_kernel(ConvParams p) 
     const T* gr = static_cast<const T*>(p.gy) + (size_t)b * p.T * p.C + c;
     T* gxr = static_cast<T*>(p.gx) + (size_t)b * p.T * p.C + c;
     const int tend = t1 + W - 1;
-    for (int t = t0; t < tend; t += kAhead) {
-      float nx[kAhead][V], ng[kAhead][V];
+    Raw<T, V> nx[kAhead], ng[kAhead];
+    const auto fetch = [&](int t) {
 #pragma unroll
       for (int a = 0; a < kAhead; ++a)
         if (t + a < tend && t + a < p.T) {
-          load_vec<T, V>(xr + (size_t)(t + a) * p.ldx, nx[a]);
-          load_vec<T, V>(gr + (size_t)(t + a) * p.C, ng[a]);
+          nx[a].load(xr + (size_t)(t + a) * p.ldx, V, true);
+          ng[a].load(gr + (size_t)(t + a) * p.C, V, true);
         }
+    };
+    fetch(t0);
+    for (int t = t0; t < tend; t += kAhead) {
+      Raw<T, V> cx[kAhead], cg[kAhead];
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a) cx[a] = nx[a], cg[a] = ng[a];
+      fetch(t + kAhead);
 #pragma unroll
       for (int a = 0; a < kAhead; ++a) {
         const int ta = t + a;
@@ -154,13 +169,13 @@ __global__ void __launch_bounds__(32 * kBwdWarps) conv_bwd_kernel(ConvParams p) 
           for (int i = 0; i < V; ++i) {
 #pragma unroll
             for (int j = 0; j < W - 1; ++j) win[j][i] = win[j + 1][i];
-            win[W - 1][i] = nx[a][i];
-            float g = ng[a][i];
+            win[W - 1][i] = cx[a][i];
+            float g = cg[a][i];
             if (p.silu) {
               float pre = bias[i];
 #pragma unroll
               for (int j = 0; j < W; ++j) pre = fmaf(w[j][i], win[j][i], pre);
-              const float s = sigmoid(pre);
+              const float s = sigmoid_ex2(pre);
               g *= s * fmaf(pre, 1.f - s, 1.f);
             }
             gp[W - 1][i] = g;
@@ -247,7 +262,7 @@ __global__ void __launch_bounds__(kThreads) conv_step_kernel(ConvParams p) {
     float acc = p.bias != nullptr ? p.bias[c + i] : 0.f;
 #pragma unroll
     for (int j = 0; j < W; ++j) acc = fmaf(p.weight[(size_t)(c + i) * W + j], win[j][i], acc);
-    o[i] = p.silu ? acc * sigmoid(acc) : acc;
+    o[i] = p.silu ? acc * sigmoid_ex2(acc) : acc;
   }
   store_vec<T, V>(static_cast<T*>(p.y) + (size_t)b * p.C + c, o);
 #pragma unroll
@@ -296,7 +311,7 @@ cudaError_t run_v(ConvPass pass, const ConvParams& p, cudaStream_t st) {
     case ConvPass::kForward:
       return p.W == 2 ? fwd_vw<T, V, 2>(p, st) : p.W == 3 ? fwd_vw<T, V, 3>(p, st) : fwd_vw<T, V, 4>(p, st);
     case ConvPass::kBackward: {
-      constexpr int VB = V == 8 ? 4 : V;
+      constexpr int VB = V > 2 ? 2 : V;
       return p.W == 2 ? bwd_vw<T, VB, 2>(p, st) : p.W == 3 ? bwd_vw<T, VB, 3>(p, st) : bwd_vw<T, VB, 4>(p, st);
     }
     case ConvPass::kStep:
@@ -313,8 +328,8 @@ int conv_bwd_parts(int B, int T) {
 }
 
 cudaError_t launch_conv(ConvPass pass, bool bf16, bool vec, const ConvParams& p, cudaStream_t st) {
-  if (bf16) return vec ? run_v<__nv_bfloat16, 8>(pass, p, st) : run_v<__nv_bfloat16, 1>(pass, p, st);
-  return vec ? run_v<float, 4>(pass, p, st) : run_v<float, 1>(pass, p, st);
+  if (bf16) return vec ? run_v<__nv_bfloat16, 4>(pass, p, st) : run_v<__nv_bfloat16, 1>(pass, p, st);
+  return vec ? run_v<float, 2>(pass, p, st) : run_v<float, 1>(pass, p, st);
 }
 
 cudaError_t launch_copy_bytes(size_t n, const void* src, void* dst, cudaStream_t st) {

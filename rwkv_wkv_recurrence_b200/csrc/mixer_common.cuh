@@ -142,14 +142,34 @@ struct Raw {
   }
 };
 
-// softplus(v) = log(1 + e^v) = max(v, 0) + log1p(e^-|v|) and its derivative, the logistic sigmoid;
-// both keep their relative accuracy for very negative v, where the step sizes of a scan lie.
-__device__ __forceinline__ float softplus(float v, float& sig) {
-  const float e = expf(-fabsf(v));
-  const float r = 1.f / (1.f + e);
-  sig = v >= 0.f ? r : e * r;
-  if (v != v) sig = v;
-  return fmaxf(v, 0.f) + log1pf(e) + (v != v ? v : 0.f);
+// Two fp32 operations in one instruction (sm_100 packed arithmetic); each half rounds as the single
+// instruction does.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<unsigned long long&>(d))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)),
+        "l"(reinterpret_cast<unsigned long long&>(c)));
+  return d;
 }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<unsigned long long&>(d))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<unsigned long long&>(d))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+  return d;
+}
+__device__ __forceinline__ float2 dup2(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 ex2_2(float2 x) { return make_float2(ex2(x.x), ex2(x.y)); }
+
+// Logistic sigmoid 1 / (1 + 2^(-x log2 e)); saturates to 0 and 1 without NaN.
+__device__ __forceinline__ float sigmoid_ex2(float x) { return rcp_approx(1.f + ex2(-kL2eHi * x)); }
 
 }  // namespace rwkv

@@ -61,11 +61,11 @@ struct TeamSum {
 template <int TS>
 constexpr int kCtaThreads = TS > 32 ? TS : 256;
 
-// Where a team works: its group, first row, row stride, and columns lane·V + k·TS·V of the group.
+// Where a team works: its group, first row, row stride.
 template <int TS>
 struct Team {
   int lane, g;
-  long long m, step;
+  long long m, step, turns;
   __device__ __forceinline__ explicit Team(const NormParams& p) {
     constexpr int PER = kCtaThreads<TS> / TS;
     lane = threadIdx.x % TS;
@@ -73,18 +73,34 @@ struct Team {
     g = (int)(id % p.G);
     m = id / p.G;
     step = p.slices;
-    if (m >= step) m = p.M;  // a team past the last slice has no rows
+    // a team past the last slice has no rows; teams of a warp's width or less share a warp with
+    // others, whose shuffles they take part in: all take as many turns as the first slice
+    turns = TS > 32 ? (p.M - m + step - 1) / step : (p.M + step - 1) / step;
+    if (m >= step) m = p.M;
   }
 };
 
-// A group's vectors k = 0 .. K-1 of this lane (zeros past column N).
+// A lane's part of a row as loaded: vectors k = 0 .. K-1 at columns (k TS + lane) V (zeros past N).
 template <typename T, int V, int K, int TS>
-__device__ __forceinline__ void load_row(const T* row, int lane, int N, float (&f)[K][V]) {
+struct RowPart {
+  Raw<T, V> v[K];
+  __device__ __forceinline__ void load(const void* base, size_t off, int lane, int N) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int col = (k * TS + lane) * V;
+      v[k].load(static_cast<const T*>(base) + off + col, col < N ? V : 0, true);
+    }
+  }
+};
+
+// Parameters of a group in the same places.
+template <int V, int K, int TS>
+__device__ __forceinline__ void load_params(const float* row, int lane, int N, float (&f)[K][V]) {
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     const int col = (k * TS + lane) * V;
-    if (col < N) {
-      load_vec<T, V>(row + col, f[k]);
+    if (row != nullptr && col < N) {
+      load_vec<float, V>(row + col, f[k]);
     } else {
 #pragma unroll
       for (int i = 0; i < V; ++i) f[k][i] = 0.f;
@@ -92,47 +108,54 @@ __device__ __forceinline__ void load_row(const T* row, int lane, int N, float (&
   }
 }
 
-// x becomes x - mean (0 past column N); returns 1 / sqrt(var + eps).
-template <int V, int K, int TS>
-__device__ __forceinline__ float center(float (&x)[K][V], int lane, int N, float inv_n, float eps, TeamSum<TS>& sum) {
+// x - mean (0 past column N); returns 1 / sqrt(var + eps).
+template <typename T, int V, int K, int TS>
+__device__ __forceinline__ float center(const RowPart<T, V, K, TS>& r, float (&x)[K][V], int lane, int N, float inv_n,
+                                        float eps, TeamSum<TS>& sum) {
   float s = 0.f;
 #pragma unroll
   for (int k = 0; k < K; ++k)
 #pragma unroll
-    for (int i = 0; i < V; ++i) s += x[k][i];
+    for (int i = 0; i < V; ++i) s += x[k][i] = r.v[k][i];
   const float mean = sum(s, 0.f).x * inv_n;
   float q = 0.f;
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    const bool in = (k * TS + lane) * V < N;
+    const float mk = (k * TS + lane) * V < N ? mean : 0.f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      x[k][i] = in ? x[k][i] - mean : 0.f;
+      x[k][i] -= mk;
       q = fmaf(x[k][i], x[k][i], q);
     }
   }
   return 1.f / sqrtf(fmaf(sum(q, 0.f).x, inv_n, eps));
 }
 
-template <typename T, int V, int K, int TS>
-__global__ void __launch_bounds__(kCtaThreads<TS>) norm_fwd_kernel(const NormParams p) {
+// Rows are fetched a turn ahead and left as loaded until they are due.
+template <typename T, int V, int K, int TS, bool GATE>
+__global__ void __launch_bounds__(kCtaThreads<TS>) norm_fwd_kernel(const __grid_constant__ NormParams p) {
   __shared__ float2 buf[2 * kMaxTeam / 32];
   TeamSum<TS> sum{buf};
-  Team<TS> tm(p);
+  const Team<TS> tm(p);
   const float inv_n = 1.f / (float)p.N;
   float w[K][V], b[K][V];
-  load_row<float, V, K, TS>(p.weight + (size_t)tm.g * p.N, tm.lane, p.N, w);
-  if (p.bias != nullptr) load_row<float, V, K, TS>(p.bias + (size_t)tm.g * p.N, tm.lane, p.N, b);
-  // teams of one warp's width or less share a warp with others: all lanes take every turn
-  const long long turns = TS > 32 ? (p.M - tm.m + tm.step - 1) / tm.step : (p.M + tm.step - 1) / tm.step;
-  for (long long it = 0; it < turns; ++it) {
-    const long long m = tm.m + it * tm.step;
+  const size_t stride = (size_t)tm.step * p.G * p.N;
+  size_t off = ((size_t)tm.m * p.G + tm.g) * p.N;
+  long long m = tm.m;
+  RowPart<T, V, K, TS> rx, rz;
+  const auto fetch = [&](size_t o, bool on) {
+    rx.load(p.x, on ? o : 0, tm.lane, on ? p.N : 0);
+    if constexpr (GATE) rz.load(p.gate, on ? o : 0, tm.lane, on ? p.N : 0);
+  };
+  fetch(off, m < p.M);
+  load_params<V, K, TS>(p.weight + (size_t)tm.g * p.N, tm.lane, p.N, w);
+  load_params<V, K, TS>(p.bias != nullptr ? p.bias + (size_t)tm.g * p.N : nullptr, tm.lane, p.N, b);
+  for (long long it = 0; it < tm.turns; ++it, m += tm.step, off += stride) {
     const bool on = m < p.M;
-    const size_t off = ((size_t)(on ? m : 0) * p.G + tm.g) * p.N;
-    float x[K][V], z[K][V];
-    load_row<T, V, K, TS>(static_cast<const T*>(p.x) + off, tm.lane, p.N, x);
-    if (p.gate != nullptr) load_row<T, V, K, TS>(static_cast<const T*>(p.gate) + off, tm.lane, p.N, z);
-    const float rstd = center<V, K, TS>(x, tm.lane, p.N, inv_n, p.eps, sum);
+    const RowPart<T, V, K, TS> cx = rx, cz = rz;
+    fetch(off + stride, m + tm.step < p.M);
+    float x[K][V];
+    const float rstd = center<T, V, K, TS>(cx, x, tm.lane, p.N, inv_n, p.eps, sum);
     if (!on) continue;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
@@ -141,51 +164,60 @@ __global__ void __launch_bounds__(kCtaThreads<TS>) norm_fwd_kernel(const NormPar
       float o[V];
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        o[i] = fmaf(x[k][i] * rstd, w[k][i], p.bias != nullptr ? b[k][i] : 0.f);
-        if (p.gate != nullptr) o[i] *= z[k][i] * sigmoid(z[k][i]);
+        o[i] = fmaf(x[k][i] * rstd, w[k][i], b[k][i]);
+        if constexpr (GATE) {
+          const float z = cz.v[k][i];
+          o[i] *= z * sigmoid_ex2(z);
+        }
       }
       store_vec<T, V>(static_cast<T*>(p.y) + off + col, o);
     }
   }
 }
 
-template <typename T, int V, int K, int TS>
-__global__ void __launch_bounds__(kCtaThreads<TS>) norm_bwd_kernel(const NormParams p) {
+template <typename T, int V, int K, int TS, bool GATE>
+__global__ void __launch_bounds__(kCtaThreads<TS>) norm_bwd_kernel(const __grid_constant__ NormParams p) {
   __shared__ float2 buf[2 * kMaxTeam / 32];
   TeamSum<TS> sum{buf};
-  Team<TS> tm(p);
+  const Team<TS> tm(p);
   const float inv_n = 1.f / (float)p.N;
   float w[K][V], b[K][V], gw[K][V], gb[K][V];
-  load_row<float, V, K, TS>(p.weight + (size_t)tm.g * p.N, tm.lane, p.N, w);
+  const size_t stride = (size_t)tm.step * p.G * p.N;
+  size_t off = ((size_t)tm.m * p.G + tm.g) * p.N;
+  long long m = tm.m;
+  RowPart<T, V, K, TS> rx, rg, rz;
+  const auto fetch = [&](size_t o, bool on) {
+    rx.load(p.x, on ? o : 0, tm.lane, on ? p.N : 0);
+    rg.load(p.gy, on ? o : 0, tm.lane, on ? p.N : 0);
+    if constexpr (GATE) rz.load(p.gate, on ? o : 0, tm.lane, on ? p.N : 0);
+  };
+  fetch(off, m < p.M);
+  load_params<V, K, TS>(p.weight + (size_t)tm.g * p.N, tm.lane, p.N, w);
+  if constexpr (GATE)
+    load_params<V, K, TS>(p.bias != nullptr ? p.bias + (size_t)tm.g * p.N : nullptr, tm.lane, p.N, b);
 #pragma unroll
   for (int k = 0; k < K; ++k)
 #pragma unroll
-    for (int i = 0; i < V; ++i) b[k][i] = gw[k][i] = gb[k][i] = 0.f;
-  if (p.bias != nullptr && p.gate != nullptr)
-    load_row<float, V, K, TS>(p.bias + (size_t)tm.g * p.N, tm.lane, p.N, b);
-  const long long turns = TS > 32 ? (p.M - tm.m + tm.step - 1) / tm.step : (p.M + tm.step - 1) / tm.step;
-  for (long long it = 0; it < turns; ++it) {
-    const long long m = tm.m + it * tm.step;
+    for (int i = 0; i < V; ++i) gw[k][i] = gb[k][i] = 0.f;
+  for (long long it = 0; it < tm.turns; ++it, m += tm.step, off += stride) {
     const bool on = m < p.M;
-    const size_t off = ((size_t)(on ? m : 0) * p.G + tm.g) * p.N;
+    const RowPart<T, V, K, TS> cx = rx, cg = rg, cz = rz;
+    fetch(off + stride, m + tm.step < p.M);
     float x[K][V], g[K][V], z[K][V];
-    load_row<T, V, K, TS>(static_cast<const T*>(p.x) + off, tm.lane, p.N, x);
-    load_row<T, V, K, TS>(static_cast<const T*>(p.gy) + off, tm.lane, p.N, g);
-    if (p.gate != nullptr) load_row<T, V, K, TS>(static_cast<const T*>(p.gate) + off, tm.lane, p.N, z);
-    const float rstd = center<V, K, TS>(x, tm.lane, p.N, inv_n, p.eps, sum);
+    const float rstd = center<T, V, K, TS>(cx, x, tm.lane, p.N, inv_n, p.eps, sum);
     float su = 0.f, sx = 0.f;
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         x[k][i] *= rstd;
-        if (p.gate != nullptr) {
-          const float s = sigmoid(z[k][i]);
-          const float gl = g[k][i];
-          g[k][i] = gl * (z[k][i] * s);
-          z[k][i] = gl * fmaf(x[k][i], w[k][i], b[k][i]) * (s * fmaf(z[k][i], 1.f - s, 1.f));
+        g[k][i] = cg.v[k][i];  // 0 in a turn without a row
+        if constexpr (GATE) {
+          const float zi = cz.v[k][i], s = sigmoid_ex2(zi), zs = zi * s, gl = g[k][i];
+          z[k][i] = gl * fmaf(x[k][i], w[k][i], b[k][i]) * fmaf(zs, 1.f - s, s);
+          g[k][i] = gl * zs;
         }
-        if (on) {
+        if (on) {  // a row that is not there has x = 0 / sqrt(eps), which eps = 0 makes a NaN
           gw[k][i] = fmaf(g[k][i], x[k][i], gw[k][i]);
           gb[k][i] += g[k][i];
         }
@@ -195,16 +227,16 @@ __global__ void __launch_bounds__(kCtaThreads<TS>) norm_bwd_kernel(const NormPar
       }
     const float2 r = sum(su, sx);
     if (!on) continue;
-    const float mu = r.x * inv_n, mx = r.y * inv_n;
+    const float c0 = -rstd * r.x * inv_n, c1 = -rstd * r.y * inv_n;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int col = (k * TS + tm.lane) * V;
       if (col >= p.N) continue;
       float o[V];
 #pragma unroll
-      for (int i = 0; i < V; ++i) o[i] = rstd * (fmaf(g[k][i], w[k][i], -mu) - x[k][i] * mx);
+      for (int i = 0; i < V; ++i) o[i] = fmaf(rstd * g[k][i], w[k][i], fmaf(c1, x[k][i], c0));
       store_vec<T, V>(static_cast<T*>(p.gx) + off + col, o);
-      if (p.gate != nullptr) store_vec<T, V>(static_cast<T*>(p.ggate) + off + col, z[k]);
+      if constexpr (GATE) store_vec<T, V>(static_cast<T*>(p.ggate) + off + col, z[k]);
     }
   }
   const long long slice = ((long long)blockIdx.x * (kCtaThreads<TS> / TS) + threadIdx.x / TS) / p.G;
@@ -249,7 +281,7 @@ __global__ void __launch_bounds__(kMaxTeam) norm_fwd_wide_kernel(const NormParam
       float o = fmaf((IO<T>::to_f(x[i]) - mean) * rstd, p.weight[col], p.bias != nullptr ? p.bias[col] : 0.f);
       if (p.gate != nullptr) {
         const float z = IO<T>::to_f(static_cast<const T*>(p.gate)[off + i]);
-        o *= z * sigmoid(z);
+        o *= z * sigmoid_ex2(z);
       }
       static_cast<T*>(p.y)[off + i] = IO<T>::from_f(o);
     }
@@ -278,7 +310,7 @@ __global__ void __launch_bounds__(kMaxTeam) norm_bwd_wide_kernel(const NormParam
       const float xh = (IO<T>::to_f(x[i]) - mean) * rstd, w = p.weight[col];
       float g = IO<T>::to_f(gy[i]);
       if (gate != nullptr) {
-        const float z = IO<T>::to_f(gate[i]), s = sigmoid(z);
+        const float z = IO<T>::to_f(gate[i]), s = sigmoid_ex2(z);
         static_cast<T*>(p.ggate)[off + i] = IO<T>::from_f(
             g * fmaf(xh, w, p.bias != nullptr ? p.bias[col] : 0.f) * (s * fmaf(z, 1.f - s, 1.f)));
         g *= z * s;
@@ -296,7 +328,7 @@ __global__ void __launch_bounds__(kMaxTeam) norm_bwd_wide_kernel(const NormParam
       float g = IO<T>::to_f(gy[i]);
       if (gate != nullptr) {
         const float z = IO<T>::to_f(gate[i]);
-        g *= z * sigmoid(z);
+        g *= z * sigmoid_ex2(z);
       }
       static_cast<T*>(p.gx)[off + i] =
           IO<T>::from_f(rstd * (fmaf(g, p.weight[(size_t)tm.g * p.N + i], -mu) - xh * mx));
@@ -304,24 +336,37 @@ __global__ void __launch_bounds__(kMaxTeam) norm_bwd_wide_kernel(const NormParam
   }
 }
 
-// gweight, gbias [C]: the slices' sums added in order.  32 columns by 8 rows of threads.
-__global__ void __launch_bounds__(256) norm_reduce_kernel(int slices, int C, const float* __restrict__ part,
-                                                          float* gweight, float* gbias) {
-  __shared__ double red[8][32];
-  const int col = blockIdx.x * 32 + (threadIdx.x & 31), r = threadIdx.x >> 5;
-  double s = 0.0;
-  if (col < 2 * C)
-    for (int k = r; k < slices; k += 8) s += (double)part[(size_t)k * 2 * C + col];
-  red[r][threadIdx.x & 31] = s;
-  __syncthreads();
-  if (r == 0 && col < 2 * C) {
-    s = 0.0;
+// gweight, gbias [C]: the slices' sums added in order: 32 columns by 32 rows of threads, a thread's
+// loads 8 at a time.
+__global__ void __launch_bounds__(1024) norm_reduce_kernel(int slices, int C, const float* __restrict__ part,
+                                                           float* gweight, float* gbias) {
+  __shared__ float red[32][33];
+  const int lane = threadIdx.x & 31, r = threadIdx.x >> 5, col = blockIdx.x * 32 + lane;
+  const size_t row = 2 * (size_t)C;
+  float s = 0.f;
+  if (col < 2 * C) {
+    const float* q = part + col;
+    int k = r;
+    for (; k + 7 * 32 < slices; k += 8 * 32) {
+      float v[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) s += red[k][threadIdx.x & 31];
-    if (col < C)
-      gweight[col] = (float)s;
+      for (int i = 0; i < 8; ++i) v[i] = q[(size_t)(k + 32 * i) * row];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s += v[i];
+    }
+    for (; k < slices; k += 32) s += q[(size_t)k * row];
+  }
+  red[r][lane] = s;
+  __syncthreads();
+  s = red[lane][r];  // column r of this CTA, row `lane`
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  const int c = blockIdx.x * 32 + r;
+  if (lane == 0 && c < 2 * C) {
+    if (c < C)
+      gweight[c] = s;
     else if (gbias != nullptr)
-      gbias[col - C] = (float)s;
+      gbias[c - C] = s;
   }
 }
 
@@ -346,10 +391,10 @@ cudaError_t run_team(const NormParams& p, cudaStream_t st) {
   constexpr int PER = kCtaThreads<TS> / TS;
   const long long teams = (long long)p.slices * p.G;
   const unsigned grid = (unsigned)((teams + PER - 1) / PER);
-  if constexpr (BWD)
-    norm_bwd_kernel<T, V, K, TS><<<grid, kCtaThreads<TS>, 0, st>>>(p);
-  else
-    norm_fwd_kernel<T, V, K, TS><<<grid, kCtaThreads<TS>, 0, st>>>(p);
+  const auto kernel =
+      BWD ? (p.gate != nullptr ? norm_bwd_kernel<T, V, K, TS, true> : norm_bwd_kernel<T, V, K, TS, false>)
+          : (p.gate != nullptr ? norm_fwd_kernel<T, V, K, TS, true> : norm_fwd_kernel<T, V, K, TS, false>);
+  kernel<<<grid, kCtaThreads<TS>, 0, st>>>(p);
   return cudaGetLastError();
 }
 
@@ -406,7 +451,7 @@ cudaError_t launch_norm_bwd(bool bf16, bool vec, const NormParams& p0, cudaStrea
   const cudaError_t e = run<true>(bf16, vec, p, st);
   if (e != cudaSuccess) return e;
   const int C = p.G * p.N;
-  norm_reduce_kernel<<<(unsigned)((2LL * C + 31) / 32), 256, 0, st>>>(p.slices, C, p.part, p.gweight, p.gbias);
+  norm_reduce_kernel<<<(unsigned)((2LL * C + 31) / 32), 1024, 0, st>>>(p.slices, C, p.part, p.gweight, p.gbias);
   return cudaGetLastError();
 }
 

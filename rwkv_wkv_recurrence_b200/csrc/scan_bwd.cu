@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, 3) scan_bwd_kernel(const __grid_cons
       float2 gpre = dup2(0.f);  // gy silu'(z)
       if (f.z != nullptr) {
         const float2 z = sm.z.pair(i);
-        const float sx = sigmoid(z.x), sy = sigmoid(z.y);
+        const float sx = sigmoid_ex2(z.x), sy = sigmoid_ex2(z.y);
         gpre = make_float2(g.x * sx * fmaf(z.x, 1.f - sx, 1.f), g.y * sy * fmaf(z.y, 1.f - sy, 1.f));
         g = make_float2(g.x * (z.x * sx), g.y * (z.y * sy));
       }

@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(Shape<N, CH_>::kThreads) scan_fwd_kernel(const
       float2 in = make_float2(dl.x * x[i], dl.y * x[i + 1]);
       if constexpr (REV) {
         in = make_float2(x[i], x[i + 1]);
-        if (p.z != nullptr) in = make_float2(x[i] * (R.z[i] * sigmoid(R.z[i])), x[i + 1] * (R.z[i + 1] * sigmoid(R.z[i + 1])));
+        if (p.z != nullptr) in = make_float2(x[i] * (R.z[i] * sigmoid_ex2(R.z[i])), x[i + 1] * (R.z[i + 1] * sigmoid_ex2(R.z[i + 1])));
       }
       const bool on0 = tact && i < nc, on1 = tact && i + 1 < nc;
       *reinterpret_cast<float4*>(&sm.dx[lt][lq * RUN + i]) =
@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(Shape<N, CH_>::kThreads) scan_fwd_kernel(const
         }
         if (p.z != nullptr) {
 #pragma unroll
-          for (int i = 0; i < RUN; ++i) o[i] *= z[i] * sigmoid(z[i]);
+          for (int i = 0; i < RUN; ++i) o[i] *= z[i] * sigmoid_ex2(z[i]);
         }
         store_part<T, RUN>(static_cast<T*>(p.y) + ((size_t)bb * p.T + ts + lt) * p.C + c0, nc, p.vec, o);
       }

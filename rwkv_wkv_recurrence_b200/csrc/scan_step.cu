@@ -29,8 +29,8 @@ __global__ void __launch_bounds__(kThreads) scan_step_kernel(const __grid_consta
   const float x = IO<T>::to_f(static_cast<const T*>(p.x)[b * p.ldx + c]);
   float v = IO<T>::to_f(static_cast<const T*>(p.dt)[b * p.lddt + c]);
   if (p.dt_bias != nullptr) v += p.dt_bias[c];
-  float sig;
-  const float delta = softplus(v, sig), dx = delta * x;
+  float2 e;
+  const float delta = softplus2(dup2(v), e).x, dx = delta * x;
   float y = 0.f;
 #pragma unroll
   for (int i = 0; i < kSN; ++i) {
@@ -45,7 +45,7 @@ __global__ void __launch_bounds__(kThreads) scan_step_kernel(const __grid_consta
     if (p.d != nullptr) y = fmaf(p.d[c], x, y);
     if (p.z != nullptr) {
       const float z = IO<T>::to_f(static_cast<const T*>(p.z)[b * p.ldz + c]);
-      y *= z * sigmoid(z);
+      y *= z * sigmoid_ex2(z);
     }
     static_cast<T*>(p.y)[b * p.C + c] = IO<T>::from_f(y);
   }
