@@ -82,7 +82,7 @@ rwkv_status rwkv_causal_conv_forward(int64_t B, int64_t T, int64_t C, int64_t W,
   p.y = y;
   p.state_in = state_in;
   p.state_out = state_out;
-  const bool vec = aligned(16, {x, y, state_in, state_out}) && vec_len(16 / (int)esz, {C, ldx});
+  const bool vec = aligned(16, {weight, x, y, state_in, state_out}) && vec_len(16 / (int)esz, {C, ldx});
   return launch_conv(ConvPass::kForward, bf16, vec, p, st) == cudaSuccess ? RWKV_OK : RWKV_ERR_CUDA;
 }
 
@@ -138,7 +138,7 @@ rwkv_status rwkv_causal_conv_backward(int64_t B, int64_t T, int64_t C, int64_t W
   p.gbias = gbias;
   p.part = static_cast<float*>(workspace);
   const bool vec =
-      aligned(16, {x, gy, gx, state_in, gstate_out, gstate_in}) && vec_len(16 / (int)esz, {C, ldx});
+      aligned(16, {weight, x, gy, gx, state_in, gstate_out, gstate_in}) && vec_len(16 / (int)esz, {C, ldx});
   return launch_conv(ConvPass::kBackward, bf16, vec, p, st) == cudaSuccess ? RWKV_OK : RWKV_ERR_CUDA;
 }
 
@@ -168,7 +168,7 @@ rwkv_status rwkv_causal_conv_step(int64_t B, int64_t C, int64_t W, rwkv_dtype dt
   p.y = y;
   p.state_in = state_in;
   p.state_out = state_out;
-  const bool vec = aligned(16, {x, y, state_in, state_out}) && vec_len(16 / (int)esz, {C, ldx});
+  const bool vec = aligned(16, {weight, x, y, state_in, state_out}) && vec_len(16 / (int)esz, {C, ldx});
   return launch_conv(ConvPass::kStep, bf16, vec, p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? RWKV_OK
              : RWKV_ERR_CUDA;

@@ -24,24 +24,71 @@ constexpr int kThreads = 128;
 constexpr int kFwdStretch = 32;  // tokens per thread, forward
 constexpr int kBwdStretch = 64;  // tokens per thread, backward
 constexpr int kBwdWarps = 8;     // stretches per CTA (their weight-gradient sums meet in shared memory)
+constexpr int kStepStreams = 2;  // streams per thread, step
 constexpr int kAhead = 8;        // tokens fetched together
+
+// Channels are worked on in pairs (packed arithmetic); with V = 1 a pair's second half is idle.
+template <int V>
+constexpr int kPairs = (V + 1) / 2;
 
 // Element of the concatenation (state, x): position k < W-1 is state row k, the rest token k-(W-1).
 template <typename T, int V, int W>
-__device__ __forceinline__ void load_pos(const ConvParams& p, int b, int k, int c, float (&f)[V]) {
+__device__ __forceinline__ void load_pos(const ConvParams& p, int b, int k, int c, float2 (&f)[kPairs<V>]) {
   const int t = k - (W - 1);
-  if (t >= 0) {
-    load_vec<T, V>(static_cast<const T*>(p.x) + ((size_t)b * p.T + t) * p.ldx + c, f);
-  } else if (p.state_in != nullptr) {
-    load_vec<T, V>(static_cast<const T*>(p.state_in) + ((size_t)b * (W - 1) + k) * p.C + c, f);
-  } else {
+  Raw<T, V> r;
+  if (t >= 0)
+    r.load(static_cast<const T*>(p.x) + ((size_t)b * p.T + t) * p.ldx + c);
+  else if (p.state_in != nullptr)
+    r.load(static_cast<const T*>(p.state_in) + ((size_t)b * (W - 1) + k) * p.C + c);
+  else
+    r.zero();
 #pragma unroll
-    for (int i = 0; i < V; ++i) f[i] = 0.f;
+  for (int i = 0; i < kPairs<V>; ++i) f[i] = r.pair(i);
+}
+
+// The filters and biases of channels c .. c + V - 1 (W V consecutive floats: wide loads where the
+// tensors are aligned for them, which V > 1 implies).
+template <int V, int W>
+__device__ __forceinline__ void load_filter(const ConvParams& p, int c, float2 (&w)[W][kPairs<V>],
+                                            float2 (&bias)[kPairs<V>]) {
+  constexpr int Q = (V * W) % 4 == 0 ? 4 : (V * W) % 2 == 0 && V > 1 ? 2 : 1;
+  float f[V * W];
+  const float* q = p.weight + (size_t)c * W;
+#pragma unroll
+  for (int i = 0; i < V * W; i += Q) {
+    if constexpr (Q == 4 && V > 1) {
+      const float4 x = *reinterpret_cast<const float4*>(q + i);
+      f[i] = x.x, f[i + 1] = x.y, f[i + 2] = x.z, f[i + 3] = x.w;
+    } else if constexpr (Q == 2) {
+      const float2 x = *reinterpret_cast<const float2*>(q + i);
+      f[i] = x.x, f[i + 1] = x.y;
+    } else {
+#pragma unroll
+      for (int e = 0; e < Q; ++e) f[i + e] = q[i + e];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kPairs<V>; ++i) {
+    const bool two = 2 * i + 1 < V;
+#pragma unroll
+    for (int j = 0; j < W; ++j) w[j][i] = make_float2(f[2 * i * W + j], two ? f[two ? (2 * i + 1) * W + j : 0] : 0.f);
+    bias[i] = dup2(0.f);
+    if (p.bias != nullptr) bias[i] = make_float2(p.bias[c + 2 * i], two ? p.bias[c + (two ? 2 * i + 1 : 0)] : 0.f);
   }
 }
 
-template <typename T, int V, int W>
-__global__ void __launch_bounds__(kThreads) conv_fwd_kernel(ConvParams p) {
+// Slides a window by one token.
+template <int W, int P>
+__device__ __forceinline__ void slide(float2 (&win)[W][P]) {
+#pragma unroll
+  for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+    for (int i = 0; i < P; ++i) win[j][i] = win[j + 1][i];
+}
+
+template <typename T, int V, int W, bool SILU>
+__global__ void __launch_bounds__(kThreads) conv_fwd_kernel(const __grid_constant__ ConvParams p) {
+  constexpr int P = kPairs<V>;
   const int ncv = p.C / V;
   const long long id = (long long)blockIdx.x * kThreads + threadIdx.x;
   const int cv = (int)(id % ncv);
@@ -51,62 +98,69 @@ __global__ void __launch_bounds__(kThreads) conv_fwd_kernel(ConvParams p) {
   if (b64 >= p.B) return;
   const int b = (int)b64, c = cv * V;
   const int t0 = seg * kFwdStretch, t1 = min(p.T, t0 + kFwdStretch);
-  float w[W][V], bias[V], win[W][V];  // win[j]: the token j - (W-1) steps from the current one
+  const T* xr = static_cast<const T*>(p.x) + ((size_t)b * p.T + t0) * p.ldx + c;
+  T* yr = static_cast<T*>(p.y) + ((size_t)b * p.T + t0) * p.C + c;
+  Raw<T, V> nx[kAhead];
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    bias[i] = p.bias != nullptr ? p.bias[c + i] : 0.f;
-#pragma unroll
-    for (int j = 0; j < W; ++j) w[j][i] = p.weight[(size_t)(c + i) * W + j];
-  }
+  for (int a = 0; a < kAhead; ++a)
+    if (t0 + a < t1) nx[a].load(xr + (size_t)a * p.ldx);
+  float2 w[W][P], bias[P], win[W][P];  // win[j]: the token j - (W-1) steps from the current one
+  load_filter<V, W>(p, c, w, bias);
 #pragma unroll
   for (int j = 0; j < W - 1; ++j) load_pos<T, V, W>(p, b, t0 + j, c, win[j + 1]);
-  const T* xr = static_cast<const T*>(p.x) + (size_t)b * p.T * p.ldx + c;
-  T* yr = static_cast<T*>(p.y) + (size_t)b * p.T * p.C + c;
-  Raw<T, V> nx[kAhead];
-  const auto fetch = [&](int t) {
+  const auto token = [&](const Raw<T, V>& x, T* y) {
+    slide(win);
+    float2 o[P];
 #pragma unroll
-    for (int a = 0; a < kAhead; ++a)
-      if (t + a < t1) nx[a].load(xr + (size_t)(t + a) * p.ldx, V, true);
+    for (int i = 0; i < P; ++i) {
+      win[W - 1][i] = x.pair(i);
+      float2 acc = bias[i];
+#pragma unroll
+      for (int j = 0; j < W; ++j) acc = fma2(w[j][i], win[j][i], acc);
+      o[i] = SILU ? mul2(acc, sigmoid2(acc)) : acc;
+    }
+    store_pairs_as<T, V>(y, o);
   };
-  fetch(t0);
   for (int t = t0; t < t1; t += kAhead) {
     Raw<T, V> cur[kAhead];
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) cur[a] = nx[a];
-    fetch(t + kAhead);
+    xr += (size_t)kAhead * p.ldx;
+    if (t + 2 * kAhead <= t1) {
 #pragma unroll
-    for (int a = 0; a < kAhead; ++a) {
-      if (t + a >= t1) break;
-      float o[V];
+      for (int a = 0; a < kAhead; ++a) nx[a].load(xr + (size_t)a * p.ldx);
+    } else {
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-#pragma unroll
-        for (int j = 0; j < W - 1; ++j) win[j][i] = win[j + 1][i];
-        win[W - 1][i] = cur[a][i];
-        float acc = bias[i];
-#pragma unroll
-        for (int j = 0; j < W; ++j) acc = fmaf(w[j][i], win[j][i], acc);
-        o[i] = p.silu ? acc * sigmoid_ex2(acc) : acc;
-      }
-      store_vec<T, V>(yr + (size_t)(t + a) * p.C, o);
+      for (int a = 0; a < kAhead; ++a)
+        if (t + kAhead + a < t1) nx[a].load(xr + (size_t)a * p.ldx);
     }
+    if (t + kAhead <= t1) {
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a) token(cur[a], yr + (size_t)a * p.C);
+    } else {
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a)
+        if (t + a < t1) token(cur[a], yr + (size_t)a * p.C);
+    }
+    yr += (size_t)kAhead * p.C;
   }
   // The state after the last token is written by the thread that read the state before the first,
   // so that both may be the same array.
   if (seg == 0 && p.state_out != nullptr) {
-    float last[W - 1][V];
+    float2 last[W - 1][P];
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) load_pos<T, V, W>(p, b, p.T + j, c, last[j]);
 #pragma unroll
     for (int j = 0; j < W - 1; ++j)
-      store_vec<T, V>(static_cast<T*>(p.state_out) + ((size_t)b * (W - 1) + j) * p.C + c, last[j]);
+      store_pairs_as<T, V>(static_cast<T*>(p.state_out) + ((size_t)b * (W - 1) + j) * p.C + c, last[j]);
   }
 }
 
 // One warp per stretch: lane = channel group.  part: [B * ceil(nseg / kBwdWarps)][W+1][C] sums of
 // the weight gradients (plane W: the bias's).
-template <typename T, int V, int W>
-__global__ void __launch_bounds__(32 * kBwdWarps) conv_bwd_kernel(ConvParams p) {
+template <typename T, int V, int W, bool SILU>
+__global__ void __launch_bounds__(32 * kBwdWarps) conv_bwd_kernel(const __grid_constant__ ConvParams p) {
+  constexpr int P = kPairs<V>;
   __shared__ float red[kBwdWarps][W + 1][32 * V];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int ncg = (p.C / V + 31) / 32;                        // channel groups of 32 V
@@ -116,107 +170,132 @@ __global__ void __launch_bounds__(32 * kBwdWarps) conv_bwd_kernel(ConvParams p) 
   const int b = (int)(rest / (unsigned)nsg), seg = (int)(rest % (unsigned)nsg) * kBwdWarps + warp;
   const int c = (cg * 32 + lane) * V;
   const bool act = c < p.C && seg < p.nseg;
-  float gw[W + 1][V];
+  float2 gw[W + 1][P];
 #pragma unroll
   for (int j = 0; j <= W; ++j)
 #pragma unroll
-    for (int i = 0; i < V; ++i) gw[j][i] = 0.f;
+    for (int i = 0; i < P; ++i) gw[j][i] = dup2(0.f);
   if (act) {
-    const int t0 = seg * kBwdStretch, t1 = min(p.T, t0 + kBwdStretch);
-    float w[W][V], bias[V], win[W][V], gp[W][V];  // gp[j]: g of the token j - (W-1) steps from the current one
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      bias[i] = p.bias != nullptr ? p.bias[c + i] : 0.f;
-#pragma unroll
-      for (int j = 0; j < W; ++j) {
-        w[j][i] = p.weight[(size_t)(c + i) * W + j];
-        gp[j][i] = 0.f;
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < W - 1; ++j) load_pos<T, V, W>(p, b, t0 + j, c, win[j + 1]);
-    const T* xr = static_cast<const T*>(p.x) + (size_t)b * p.T * p.ldx + c;
-    const T* gr = static_cast<const T*>(p.gy) + (size_t)b * p.T * p.C + c;
-    T* gxr = static_cast<T*>(p.gx) + (size_t)b * p.T * p.C + c;
-    const int tend = t1 + W - 1;
+    // g_t is needed for the stretch's tokens and the W-1 behind them (0 past the end of the sequence)
+    const int t0 = seg * kBwdStretch, t1 = min(p.T, t0 + kBwdStretch), tend = t1 + W - 1;
+    float2 w[W][P], bias[P], win[W][P], gp[W][P];  // gp[j]: g of the token j - (W-1) steps from the current one
+    const T* xr = static_cast<const T*>(p.x) + ((size_t)b * p.T + t0) * p.ldx + c;
+    const T* gr = static_cast<const T*>(p.gy) + ((size_t)b * p.T + t0) * p.C + c;
+    T* gxr = static_cast<T*>(p.gx) + ((size_t)b * p.T + t0) * p.C + c;  // of the token being fetched for
     Raw<T, V> nx[kAhead], ng[kAhead];
-    const auto fetch = [&](int t) {
+    const auto fetch = [&](int t) {  // tokens t .. t + kAhead - 1, xr and gr pointing at the first
+      if (t + kAhead <= p.T) {
 #pragma unroll
-      for (int a = 0; a < kAhead; ++a)
-        if (t + a < tend && t + a < p.T) {
-          nx[a].load(xr + (size_t)(t + a) * p.ldx, V, true);
-          ng[a].load(gr + (size_t)(t + a) * p.C, V, true);
+        for (int a = 0; a < kAhead; ++a) {
+          nx[a].load(xr + (size_t)a * p.ldx);
+          ng[a].load(gr + (size_t)a * p.C);
         }
+      } else {
+#pragma unroll
+        for (int a = 0; a < kAhead; ++a)
+          if (t + a < p.T) {
+            nx[a].load(xr + (size_t)a * p.ldx);
+            ng[a].load(gr + (size_t)a * p.C);
+          }
+      }
     };
     fetch(t0);
-    for (int t = t0; t < tend; t += kAhead) {
-      Raw<T, V> cx[kAhead], cg[kAhead];
+    load_filter<V, W>(p, c, w, bias);
 #pragma unroll
-      for (int a = 0; a < kAhead; ++a) cx[a] = nx[a], cg[a] = ng[a];
-      fetch(t + kAhead);
+    for (int j = 0; j < W; ++j)
 #pragma unroll
-      for (int a = 0; a < kAhead; ++a) {
-        const int ta = t + a;
-        if (ta >= tend) break;
+      for (int i = 0; i < P; ++i) gp[j][i] = dup2(0.f);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
+    for (int j = 0; j < W - 1; ++j) load_pos<T, V, W>(p, b, t0 + j, c, win[j + 1]);
+
+    // g of one token; its part of the weight gradients when the stretch owns it
+    const auto grad = [&](const Raw<T, V>& x, const Raw<T, V>& gy, bool own) {
+      slide(gp);
+      slide(win);
 #pragma unroll
-          for (int j = 0; j < W - 1; ++j) gp[j][i] = gp[j + 1][i];
-          gp[W - 1][i] = 0.f;
+      for (int i = 0; i < P; ++i) {
+        win[W - 1][i] = x.pair(i);
+        float2 g = gy.pair(i);
+        if constexpr (SILU) {
+          float2 pre = bias[i];
+#pragma unroll
+          for (int j = 0; j < W; ++j) pre = fma2(w[j][i], win[j][i], pre);
+          const float2 s = sigmoid2(pre);
+          g = mul2(mul2(g, s), fma2(pre, fma2(s, dup2(-1.f), dup2(1.f)), dup2(1.f)));
         }
-        if (ta < p.T) {
+        gp[W - 1][i] = g;
+        if (own) {
 #pragma unroll
-          for (int i = 0; i < V; ++i) {
-#pragma unroll
-            for (int j = 0; j < W - 1; ++j) win[j][i] = win[j + 1][i];
-            win[W - 1][i] = cx[a][i];
-            float g = cg[a][i];
-            if (p.silu) {
-              float pre = bias[i];
-#pragma unroll
-              for (int j = 0; j < W; ++j) pre = fmaf(w[j][i], win[j][i], pre);
-              const float s = sigmoid_ex2(pre);
-              g *= s * fmaf(pre, 1.f - s, 1.f);
-            }
-            gp[W - 1][i] = g;
-            if (ta < t1) {
-#pragma unroll
-              for (int j = 0; j < W; ++j) gw[j][i] = fmaf(g, win[j][i], gw[j][i]);
-              gw[W][i] += g;
-            }
-          }
-        }
-        // the gradient of token ta - (W-1), or of a row of the state where that is negative; its
-        // stretch owns it when it is not before t0 (the first stretch owns the state)
-        const int to = ta - (W - 1);
-        if (to >= t0 || (seg == 0 && p.gstate_in != nullptr)) {
-          float o[V], e[V];
-          const int k = to + W - 1 - p.T;  // its row of the final state, when >= 0
-          if (k >= 0 && p.gstate_out != nullptr) {
-            load_vec<T, V>(static_cast<const T*>(p.gstate_out) + ((size_t)b * (W - 1) + k) * p.C + c, e);
-          } else {
-#pragma unroll
-            for (int i = 0; i < V; ++i) e[i] = 0.f;
-          }
-#pragma unroll
-          for (int i = 0; i < V; ++i) {
-            float acc = e[i];
-#pragma unroll
-            for (int j = 0; j < W; ++j) acc = fmaf(w[j][i], gp[W - 1 - j][i], acc);
-            o[i] = acc;
-          }
-          if (to >= 0)
-            store_vec<T, V>(gxr + (size_t)to * p.C, o);
-          else
-            store_vec<T, V>(static_cast<T*>(p.gstate_in) + ((size_t)b * (W - 1) + to + W - 1) * p.C + c, o);
+          for (int j = 0; j < W; ++j) gw[j][i] = fma2(g, win[j][i], gw[j][i]);
+          gw[W][i] = add2(g, gw[W][i]);
         }
       }
+    };
+    // gx of the token W-1 before the current one, on top of e
+    const auto back = [&](float2 (&e)[P]) {
+#pragma unroll
+      for (int i = 0; i < P; ++i)
+#pragma unroll
+        for (int j = 0; j < W; ++j) e[i] = fma2(w[j][i], gp[W - 1 - j][i], e[i]);
+    };
+    for (int t = t0; t < tend; t += kAhead) {
+      Raw<T, V> cx[kAhead], cg_[kAhead];
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a) cx[a] = nx[a], cg_[a] = ng[a];
+      xr += (size_t)kAhead * p.ldx;
+      gr += (size_t)kAhead * p.C;
+      if (t + kAhead < tend) fetch(t + kAhead);
+      if (t - (W - 1) >= t0 && t + kAhead <= t1) {
+        // all tokens owned, none before the stretch
+#pragma unroll
+        for (int a = 0; a < kAhead; ++a) {
+          grad(cx[a], cg_[a], true);
+          float2 o[P];
+#pragma unroll
+          for (int i = 0; i < P; ++i) o[i] = dup2(0.f);
+          back(o);
+          store_pairs_as<T, V>(gxr + (ptrdiff_t)(a - (W - 1)) * p.C, o);
+        }
+      } else {
+#pragma unroll
+        for (int a = 0; a < kAhead; ++a) {
+          const int ta = t + a;
+          if (ta >= tend) break;
+          if (ta < p.T) {
+            grad(cx[a], cg_[a], ta < t1);
+          } else {
+            slide(gp);
+#pragma unroll
+            for (int i = 0; i < P; ++i) gp[W - 1][i] = dup2(0.f);
+          }
+          // token ta - (W-1), or a row of the state where that is negative; its stretch owns it when it
+          // is not before t0 (the first stretch owns the state)
+          const int to = ta - (W - 1);
+          if (to >= t0 || (seg == 0 && p.gstate_in != nullptr)) {
+            float2 o[P];
+            const int k = to + W - 1 - p.T;  // its row of the final state, when >= 0
+            Raw<T, V> e;
+            if (k >= 0 && p.gstate_out != nullptr)
+              e.load(static_cast<const T*>(p.gstate_out) + ((size_t)b * (W - 1) + k) * p.C + c);
+            else
+              e.zero();
+#pragma unroll
+            for (int i = 0; i < P; ++i) o[i] = e.pair(i);
+            back(o);
+            if (to >= 0)
+              store_pairs_as<T, V>(gxr + (ptrdiff_t)(a - (W - 1)) * p.C, o);
+            else
+              store_pairs_as<T, V>(static_cast<T*>(p.gstate_in) + ((size_t)b * (W - 1) + to + W - 1) * p.C + c, o);
+          }
+        }
+      }
+      gxr += (size_t)kAhead * p.C;
     }
   }
 #pragma unroll
   for (int j = 0; j <= W; ++j)
 #pragma unroll
-    for (int i = 0; i < V; ++i) red[warp][j][lane * V + i] = gw[j][i];
+    for (int i = 0; i < V; ++i) red[warp][j][lane * V + i] = i & 1 ? gw[j][i / 2].y : gw[j][i / 2].x;
   __syncthreads();
   float* part = p.part + (size_t)rest * (W + 1) * p.C;
   for (int i = threadIdx.x; i < (W + 1) * 32 * V; i += 32 * kBwdWarps) {
@@ -229,45 +308,77 @@ __global__ void __launch_bounds__(32 * kBwdWarps) conv_bwd_kernel(ConvParams p) 
   }
 }
 
-// gweight[c][j] and gbias[c]: the parts summed in order (fp64: their number grows with the batch).
-__global__ void __launch_bounds__(kThreads) conv_reduce_kernel(int nparts, int C, int W, const float* __restrict__ part,
-                                                               float* gweight, float* gbias) {
+// gweight[c][j] and gbias[c]: the parts summed in order, 32 columns by 8 rows of threads, a thread's
+// loads 4 at a time.
+__global__ void __launch_bounds__(256) conv_reduce_kernel(int nparts, int C, int W, const float* __restrict__ part,
+                                                          float* gweight, float* gbias) {
+  __shared__ float red[8][32];
   const size_t n = (size_t)(W + 1) * C;
-  const size_t i = (size_t)blockIdx.x * kThreads + threadIdx.x;
-  if (i >= n) return;
-  double s = 0.0;
-  for (int k = 0; k < nparts; ++k) s += (double)part[(size_t)k * n + i];
+  const int lane = threadIdx.x & 31, r = threadIdx.x >> 5;
+  const size_t i = (size_t)blockIdx.x * 32 + lane;
+  float s = 0.f;
+  if (i < n) {
+    const float* q = part + i;
+    int k = r;
+    for (; k + 3 * 8 < nparts; k += 4 * 8) {
+      const float a = q[(size_t)k * n], b = q[(size_t)(k + 8) * n], c = q[(size_t)(k + 16) * n],
+                  d = q[(size_t)(k + 24) * n];
+      s += (a + b) + (c + d);
+    }
+    for (; k < nparts; k += 8) s += q[(size_t)k * n];
+  }
+  red[r][lane] = s;
+  __syncthreads();
+  if (r != 0 || i >= n) return;
+#pragma unroll
+  for (int k = 1; k < 8; ++k) s += red[k][lane];
   const int j = (int)(i / C), c = (int)(i % C);
   if (j < W)
-    gweight[(size_t)c * W + j] = (float)s;
+    gweight[(size_t)c * W + j] = s;
   else if (gbias != nullptr)
-    gbias[c] = (float)s;
+    gbias[c] = s;
 }
 
 // One token per stream: the window is the state's rows and the token; the rows move up by one.  A
-// thread reads every row of its channels before it writes one, so state_out may be state_in.
+// thread reads every row of its channels before it writes one, so state_out may be state_in.  It
+// takes kStepStreams streams, whose loads are in flight together and share the filters.
 template <typename T, int V, int W>
-__global__ void __launch_bounds__(kThreads) conv_step_kernel(ConvParams p) {
+__global__ void __launch_bounds__(kThreads) conv_step_kernel(const __grid_constant__ ConvParams p) {
+  constexpr int P = kPairs<V>;
   const int ncv = p.C / V;
   const long long id = (long long)blockIdx.x * kThreads + threadIdx.x;
-  const long long b = id / ncv;
-  if (b >= p.B) return;
-  const int c = (int)(id % ncv) * V;
-  float win[W][V], o[V];
+  const long long b0 = id / ncv * kStepStreams;
+  if (b0 >= p.B) return;
+  const int c = (int)(id % ncv) * V, nb = (int)min((long long)kStepStreams, p.B - b0);
+  float2 win[kStepStreams][W][P], w[W][P], bias[P];
 #pragma unroll
-  for (int j = 0; j < W - 1; ++j) load_pos<T, V, W>(p, (int)b, j, c, win[j]);
-  load_vec<T, V>(static_cast<const T*>(p.x) + (size_t)b * p.ldx + c, win[W - 1]);
+  for (int k = 0; k < kStepStreams; ++k) {
+    const int b = (int)b0 + (k < nb ? k : 0);
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    float acc = p.bias != nullptr ? p.bias[c + i] : 0.f;
+    for (int j = 0; j < W - 1; ++j) load_pos<T, V, W>(p, b, j, c, win[k][j]);
+    Raw<T, V> x;
+    x.load(static_cast<const T*>(p.x) + (size_t)b * p.ldx + c);
 #pragma unroll
-    for (int j = 0; j < W; ++j) acc = fmaf(p.weight[(size_t)(c + i) * W + j], win[j][i], acc);
-    o[i] = p.silu ? acc * sigmoid_ex2(acc) : acc;
+    for (int i = 0; i < P; ++i) win[k][W - 1][i] = x.pair(i);
   }
-  store_vec<T, V>(static_cast<T*>(p.y) + (size_t)b * p.C + c, o);
+  load_filter<V, W>(p, c, w, bias);
 #pragma unroll
-  for (int j = 0; j < W - 1; ++j)
-    store_vec<T, V>(static_cast<T*>(p.state_out) + ((size_t)b * (W - 1) + j) * p.C + c, win[j + 1]);
+  for (int k = 0; k < kStepStreams; ++k) {
+    if (k >= nb) break;
+    const size_t b = (size_t)b0 + k;
+    float2 o[P];
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      float2 acc = bias[i];
+#pragma unroll
+      for (int j = 0; j < W; ++j) acc = fma2(w[j][i], win[k][j][i], acc);
+      o[i] = p.silu ? mul2(acc, sigmoid2(acc)) : acc;
+    }
+    store_pairs_as<T, V>(static_cast<T*>(p.y) + b * p.C + c, o);
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j)
+      store_pairs_as<T, V>(static_cast<T*>(p.state_out) + (b * (W - 1) + j) * p.C + c, win[k][j + 1]);
+  }
 }
 
 // T = 0: the final state is the first (and its gradient passes through).
@@ -280,7 +391,8 @@ template <typename T, int V, int W>
 cudaError_t fwd_vw(ConvParams p, cudaStream_t st) {
   p.nseg = (p.T + kFwdStretch - 1) / kFwdStretch;
   const long long n = (long long)p.B * p.nseg * (p.C / V);
-  conv_fwd_kernel<T, V, W><<<(unsigned)((n + kThreads - 1) / kThreads), kThreads, 0, st>>>(p);
+  const auto kernel = p.silu ? conv_fwd_kernel<T, V, W, true> : conv_fwd_kernel<T, V, W, false>;
+  kernel<<<(unsigned)((n + kThreads - 1) / kThreads), kThreads, 0, st>>>(p);
   return cudaGetLastError();
 }
 
@@ -289,18 +401,18 @@ cudaError_t bwd_vw(ConvParams p, cudaStream_t st) {
   p.nseg = (p.T + kBwdStretch - 1) / kBwdStretch;
   const int nparts = conv_bwd_parts(p.B, p.T);
   const int ncg = (p.C / V + 31) / 32;
-  conv_bwd_kernel<T, V, W><<<(unsigned)nparts * (unsigned)ncg, 32 * kBwdWarps, 0, st>>>(p);
+  const auto kernel = p.silu ? conv_bwd_kernel<T, V, W, true> : conv_bwd_kernel<T, V, W, false>;
+  kernel<<<(unsigned)nparts * (unsigned)ncg, 32 * kBwdWarps, 0, st>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const size_t n = (size_t)(W + 1) * p.C;
-  conv_reduce_kernel<<<(unsigned)((n + kThreads - 1) / kThreads), kThreads, 0, st>>>(nparts, p.C, W, p.part,
-                                                                                    p.gweight, p.gbias);
+  conv_reduce_kernel<<<(unsigned)((n + 31) / 32), 256, 0, st>>>(nparts, p.C, W, p.part, p.gweight, p.gbias);
   return cudaGetLastError();
 }
 
 template <typename T, int V, int W>
 cudaError_t step_vw(const ConvParams& p, cudaStream_t st) {
-  const long long n = (long long)p.B * (p.C / V);
+  const long long n = ((long long)p.B + kStepStreams - 1) / kStepStreams * (p.C / V);
   conv_step_kernel<T, V, W><<<(unsigned)((n + kThreads - 1) / kThreads), kThreads, 0, st>>>(p);
   return cudaGetLastError();
 }

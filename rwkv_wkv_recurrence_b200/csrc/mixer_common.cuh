@@ -106,21 +106,7 @@ struct Raw {
   // The first n of the V elements at p (the rest zero); `vec` as in load_part.
   __device__ __forceinline__ void load(const T* p, int n, bool vec) {
     if (vec && n >= V) {
-      if constexpr (kBytes % 16 == 0) {
-#pragma unroll
-        for (int i = 0; i < kBytes / 16; ++i) {
-          const uint4 x = reinterpret_cast<const uint4*>(p)[i];
-          w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
-        }
-      } else if constexpr (kBytes == 8) {
-        const uint2 x = *reinterpret_cast<const uint2*>(p);
-        w[0] = x.x, w[1] = x.y;
-      } else if constexpr (kBytes == 4) {
-        w[0] = *reinterpret_cast<const uint32_t*>(p);
-      } else {
-        static_assert(kBytes == 2, "vector width");
-        w[0] = *reinterpret_cast<const unsigned short*>(p);
-      }
+      load(p);
     } else {
 #pragma unroll
       for (int i = 0; i < (kBytes + 3) / 4; ++i) w[i] = 0u;
@@ -133,6 +119,32 @@ struct Raw {
           w[i / 2] |= (uint32_t) reinterpret_cast<const unsigned short*>(p)[i] << (16 * (i & 1));
       }
     }
+  }
+  // All V elements (aligned for wide accesses, or V = 1).
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (kBytes % 16 == 0) {
+#pragma unroll
+      for (int i = 0; i < kBytes / 16; ++i) {
+        const uint4 x = reinterpret_cast<const uint4*>(p)[i];
+        w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
+      }
+    } else if constexpr (kBytes == 8) {
+      const uint2 x = *reinterpret_cast<const uint2*>(p);
+      w[0] = x.x, w[1] = x.y;
+    } else if constexpr (kBytes == 4) {
+      w[0] = *reinterpret_cast<const uint32_t*>(p);
+    } else {
+      static_assert(kBytes == 2, "vector width");
+      w[0] = *reinterpret_cast<const unsigned short*>(p);
+    }
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < (kBytes + 3) / 4; ++i) w[i] = 0u;
+  }
+  // Elements 2 i and 2 i + 1 (0 behind the last).
+  __device__ __forceinline__ float2 pair(int i) const {
+    return make_float2((*this)[2 * i], 2 * i + 1 < V ? (*this)[2 * i + 1] : 0.f);
   }
   __device__ __forceinline__ float operator[](int i) const {
     if constexpr (sizeof(T) == 4)
@@ -168,6 +180,20 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 }
 __device__ __forceinline__ float2 dup2(float x) { return make_float2(x, x); }
 __device__ __forceinline__ float2 ex2_2(float2 x) { return make_float2(ex2(x.x), ex2(x.y)); }
+
+__device__ __forceinline__ float2 sigmoid2(float2 x) {
+  const float2 e = ex2_2(mul2(x, dup2(-kL2eHi)));
+  const float2 d = add2(e, dup2(1.f));
+  return make_float2(rcp_approx(d.x), rcp_approx(d.y));
+}
+// V elements held as pairs, rounded once each.
+template <typename T, int V>
+__device__ __forceinline__ void store_pairs_as(T* p, const float2 (&v)[(V + 1) / 2]) {
+  float f[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) f[i] = i & 1 ? v[i / 2].y : v[i / 2].x;
+  store_vec<T, V>(p, f);
+}
 
 // Logistic sigmoid 1 / (1 + 2^(-x log2 e)); saturates to 0 and 1 without NaN.
 __device__ __forceinline__ float sigmoid_ex2(float x) { return rcp_approx(1.f + ex2(-kL2eHi * x)); }

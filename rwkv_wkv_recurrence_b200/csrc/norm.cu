@@ -28,18 +28,19 @@ namespace {
 constexpr int kMaxTeam = 512;
 constexpr int kTargetThreads = 148 * 1536;  // threads a launch aims at (three quarters of what the SMs hold)
 
-// Sums a and b over a team; every thread gets them.  Teams wider than a warp are whole CTAs; `buf`
-// alternates between two halves, so one barrier a call is enough.
+// Sums over a team, for all its threads: one value, or two.  Teams wider than a warp are whole CTAs;
+// `buf` alternates between two halves, so one barrier a call is enough.
 template <int TS>
 struct TeamSum {
   float2* buf;
   int phase = 0;
-  __device__ __forceinline__ float2 operator()(float a, float b) {
+  template <bool TWO>
+  __device__ __forceinline__ float2 run(float a, float b) {
     constexpr int W = TS < 32 ? TS : 32;
 #pragma unroll
     for (int o = W / 2; o > 0; o >>= 1) {
       a += __shfl_xor_sync(0xffffffffu, a, o);
-      b += __shfl_xor_sync(0xffffffffu, b, o);
+      if (TWO) b += __shfl_xor_sync(0xffffffffu, b, o);
     }
     if constexpr (TS > 32) {
       constexpr int NW = TS / 32;
@@ -51,11 +52,13 @@ struct TeamSum {
 #pragma unroll
       for (int i = 0; i < NW; ++i) {
         a += s[i].x;
-        b += s[i].y;
+        if (TWO) b += s[i].y;
       }
     }
     return make_float2(a, b);
   }
+  __device__ __forceinline__ float operator()(float a) { return run<false>(a, 0.f).x; }
+  __device__ __forceinline__ float2 operator()(float a, float b) { return run<true>(a, b); }
 };
 
 template <int TS>
@@ -80,174 +83,219 @@ struct Team {
   }
 };
 
-// A lane's part of a row as loaded: vectors k = 0 .. K-1 at columns (k TS + lane) V (zeros past N).
+// A lane's part of a row as loaded: vectors k = 0 .. K-1 at columns (k TS + lane) V; those past
+// column N stay zero.
 template <typename T, int V, int K, int TS>
 struct RowPart {
   Raw<T, V> v[K];
-  __device__ __forceinline__ void load(const void* base, size_t off, int lane, int N) {
+  __device__ __forceinline__ void zero() {
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int col = (k * TS + lane) * V;
-      v[k].load(static_cast<const T*>(base) + off + col, col < N ? V : 0, true);
-    }
+    for (int k = 0; k < K; ++k) v[k].zero();
+  }
+  __device__ __forceinline__ void load(const T* lane0, const bool (&in)[K]) {  // lane0: the lane's first column
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+      if (in[k]) v[k].load(lane0 + k * TS * V);
   }
 };
 
-// Parameters of a group in the same places.
+// Parameters of a group in the same places, in pairs (with V = 1 a pair's second half is idle).
 template <int V, int K, int TS>
-__device__ __forceinline__ void load_params(const float* row, int lane, int N, float (&f)[K][V]) {
+__device__ __forceinline__ void load_params(const float* row, int lane, const bool (&in)[K],
+                                            float2 (&f)[K][(V + 1) / 2]) {
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    const int col = (k * TS + lane) * V;
-    if (row != nullptr && col < N) {
-      load_vec<float, V>(row + col, f[k]);
-    } else {
+    Raw<float, V> r;
+    r.zero();
+    if (row != nullptr && in[k]) r.load(row + (k * TS + lane) * V);
 #pragma unroll
-      for (int i = 0; i < V; ++i) f[k][i] = 0.f;
-    }
+    for (int i = 0; i < (V + 1) / 2; ++i) f[k][i] = r.pair(i);
   }
 }
 
 // x - mean (0 past column N); returns 1 / sqrt(var + eps).
 template <typename T, int V, int K, int TS>
-__device__ __forceinline__ float center(const RowPart<T, V, K, TS>& r, float (&x)[K][V], int lane, int N, float inv_n,
-                                        float eps, TeamSum<TS>& sum) {
-  float s = 0.f;
+__device__ __forceinline__ float center(const RowPart<T, V, K, TS>& r, float2 (&x)[K][(V + 1) / 2],
+                                        const bool (&in)[K], float inv_n, float eps, TeamSum<TS>& sum) {
+  constexpr int P = (V + 1) / 2;
+  float2 s = dup2(0.f);
 #pragma unroll
   for (int k = 0; k < K; ++k)
 #pragma unroll
-    for (int i = 0; i < V; ++i) s += x[k][i] = r.v[k][i];
-  const float mean = sum(s, 0.f).x * inv_n;
-  float q = 0.f;
+    for (int i = 0; i < P; ++i) s = add2(s, x[k][i] = r.v[k].pair(i));
+  const float mean = sum(s.x + s.y) * inv_n;
+  float2 q = dup2(0.f);
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    const float mk = (k * TS + lane) * V < N ? mean : 0.f;
+    const float mk = in[k] ? -mean : 0.f;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      x[k][i] -= mk;
-      q = fmaf(x[k][i], x[k][i], q);
+    for (int i = 0; i < P; ++i) {
+      x[k][i] = add2(x[k][i], make_float2(mk, V == 1 ? 0.f : mk));
+      q = fma2(x[k][i], x[k][i], q);
     }
   }
-  return 1.f / sqrtf(fmaf(sum(q, 0.f).x, inv_n, eps));
+  return rsqrtf(fmaf(sum(q.x + q.y), inv_n, eps));
 }
 
-// Rows are fetched a turn ahead and left as loaded until they are due.
+// Rows are fetched a turn ahead and left as loaded until they are due; behind the last row the last
+// fetch is repeated and not used.
 template <typename T, int V, int K, int TS, bool GATE>
 __global__ void __launch_bounds__(kCtaThreads<TS>) norm_fwd_kernel(const __grid_constant__ NormParams p) {
+  constexpr int P = (V + 1) / 2;
   __shared__ float2 buf[2 * kMaxTeam / 32];
   TeamSum<TS> sum{buf};
   const Team<TS> tm(p);
   const float inv_n = 1.f / (float)p.N;
-  float w[K][V], b[K][V];
-  const size_t stride = (size_t)tm.step * p.G * p.N;
-  size_t off = ((size_t)tm.m * p.G + tm.g) * p.N;
+  bool in[K];
+#pragma unroll
+  for (int k = 0; k < K; ++k) in[k] = (k * TS + tm.lane) * V < p.N;
+  const ptrdiff_t stride = (ptrdiff_t)tm.step * p.G * p.N;
+  const size_t off = ((size_t)(tm.m < p.M ? tm.m : 0) * p.G + tm.g) * p.N + tm.lane * V;
+  const T* x_at = static_cast<const T*>(p.x) + off;
+  const T* z_at = GATE ? static_cast<const T*>(p.gate) + off : nullptr;
+  T* y_at = static_cast<T*>(p.y) + off;
   long long m = tm.m;
   RowPart<T, V, K, TS> rx, rz;
-  const auto fetch = [&](size_t o, bool on) {
-    rx.load(p.x, on ? o : 0, tm.lane, on ? p.N : 0);
-    if constexpr (GATE) rz.load(p.gate, on ? o : 0, tm.lane, on ? p.N : 0);
-  };
-  fetch(off, m < p.M);
-  load_params<V, K, TS>(p.weight + (size_t)tm.g * p.N, tm.lane, p.N, w);
-  load_params<V, K, TS>(p.bias != nullptr ? p.bias + (size_t)tm.g * p.N : nullptr, tm.lane, p.N, b);
-  for (long long it = 0; it < tm.turns; ++it, m += tm.step, off += stride) {
+  rx.zero();
+  rx.load(x_at, in);
+  if constexpr (GATE) {
+    rz.zero();
+    rz.load(z_at, in);
+  }
+  float2 w[K][P], b[K][P];
+  load_params<V, K, TS>(p.weight + (size_t)tm.g * p.N, tm.lane, in, w);
+  load_params<V, K, TS>(p.bias != nullptr ? p.bias + (size_t)tm.g * p.N : nullptr, tm.lane, in, b);
+  for (long long it = 0; it < tm.turns; ++it) {
     const bool on = m < p.M;
     const RowPart<T, V, K, TS> cx = rx, cz = rz;
-    fetch(off + stride, m + tm.step < p.M);
-    float x[K][V];
-    const float rstd = center<T, V, K, TS>(cx, x, tm.lane, p.N, inv_n, p.eps, sum);
-    if (!on) continue;
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int col = (k * TS + tm.lane) * V;
-      if (col >= p.N) continue;
-      float o[V];
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        o[i] = fmaf(x[k][i] * rstd, w[k][i], b[k][i]);
-        if constexpr (GATE) {
-          const float z = cz.v[k][i];
-          o[i] *= z * sigmoid_ex2(z);
-        }
+    m += tm.step;
+    if (m < p.M) {
+      x_at += stride;
+      rx.load(x_at, in);
+      if constexpr (GATE) {
+        z_at += stride;
+        rz.load(z_at, in);
       }
-      store_vec<T, V>(static_cast<T*>(p.y) + off + col, o);
     }
+    float2 x[K][P];
+    const float2 rstd = dup2(center<T, V, K, TS>(cx, x, in, inv_n, p.eps, sum));
+    if (on) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        if (!in[k]) continue;
+        float2 o[P];
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+          o[i] = fma2(mul2(x[k][i], rstd), w[k][i], b[k][i]);
+          if constexpr (GATE) {
+            const float2 z = cz.v[k].pair(i);
+            o[i] = mul2(o[i], mul2(z, sigmoid2(z)));
+          }
+        }
+        store_pairs_as<T, V>(y_at + k * TS * V, o);
+      }
+    }
+    y_at += stride;
   }
 }
 
 template <typename T, int V, int K, int TS, bool GATE>
 __global__ void __launch_bounds__(kCtaThreads<TS>) norm_bwd_kernel(const __grid_constant__ NormParams p) {
+  constexpr int P = (V + 1) / 2;
   __shared__ float2 buf[2 * kMaxTeam / 32];
   TeamSum<TS> sum{buf};
   const Team<TS> tm(p);
   const float inv_n = 1.f / (float)p.N;
-  float w[K][V], b[K][V], gw[K][V], gb[K][V];
-  const size_t stride = (size_t)tm.step * p.G * p.N;
-  size_t off = ((size_t)tm.m * p.G + tm.g) * p.N;
+  bool in[K];
+#pragma unroll
+  for (int k = 0; k < K; ++k) in[k] = (k * TS + tm.lane) * V < p.N;
+  const ptrdiff_t stride = (ptrdiff_t)tm.step * p.G * p.N;
+  const size_t off = ((size_t)(tm.m < p.M ? tm.m : 0) * p.G + tm.g) * p.N + tm.lane * V;
+  const T* x_at = static_cast<const T*>(p.x) + off;
+  const T* g_at = static_cast<const T*>(p.gy) + off;
+  const T* z_at = GATE ? static_cast<const T*>(p.gate) + off : nullptr;
+  T* gx_at = static_cast<T*>(p.gx) + off;
+  T* gz_at = GATE ? static_cast<T*>(p.ggate) + off : nullptr;
   long long m = tm.m;
   RowPart<T, V, K, TS> rx, rg, rz;
-  const auto fetch = [&](size_t o, bool on) {
-    rx.load(p.x, on ? o : 0, tm.lane, on ? p.N : 0);
-    rg.load(p.gy, on ? o : 0, tm.lane, on ? p.N : 0);
-    if constexpr (GATE) rz.load(p.gate, on ? o : 0, tm.lane, on ? p.N : 0);
-  };
-  fetch(off, m < p.M);
-  load_params<V, K, TS>(p.weight + (size_t)tm.g * p.N, tm.lane, p.N, w);
+  rx.zero();
+  rx.load(x_at, in);
+  rg.zero();
+  rg.load(g_at, in);
+  if constexpr (GATE) {
+    rz.zero();
+    rz.load(z_at, in);
+  }
+  float2 w[K][P], b[K][P], gw[K][P], gb[K][P];
+  load_params<V, K, TS>(p.weight + (size_t)tm.g * p.N, tm.lane, in, w);
   if constexpr (GATE)
-    load_params<V, K, TS>(p.bias != nullptr ? p.bias + (size_t)tm.g * p.N : nullptr, tm.lane, p.N, b);
+    load_params<V, K, TS>(p.bias != nullptr ? p.bias + (size_t)tm.g * p.N : nullptr, tm.lane, in, b);
 #pragma unroll
   for (int k = 0; k < K; ++k)
 #pragma unroll
-    for (int i = 0; i < V; ++i) gw[k][i] = gb[k][i] = 0.f;
-  for (long long it = 0; it < tm.turns; ++it, m += tm.step, off += stride) {
+    for (int i = 0; i < P; ++i) gw[k][i] = gb[k][i] = dup2(0.f);
+  for (long long it = 0; it < tm.turns; ++it) {
     const bool on = m < p.M;
     const RowPart<T, V, K, TS> cx = rx, cg = rg, cz = rz;
-    fetch(off + stride, m + tm.step < p.M);
-    float x[K][V], g[K][V], z[K][V];
-    const float rstd = center<T, V, K, TS>(cx, x, tm.lane, p.N, inv_n, p.eps, sum);
-    float su = 0.f, sx = 0.f;
+    m += tm.step;
+    if (m < p.M) {
+      x_at += stride;
+      g_at += stride;
+      rx.load(x_at, in);
+      rg.load(g_at, in);
+      if constexpr (GATE) {
+        z_at += stride;
+        rz.load(z_at, in);
+      }
+    }
+    float2 x[K][P], u[K][P], z[K][P];
+    const float rstd = center<T, V, K, TS>(cx, x, in, inv_n, p.eps, sum);
+    float2 su = dup2(0.f), sx = dup2(0.f);
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        x[k][i] *= rstd;
-        g[k][i] = cg.v[k][i];  // 0 in a turn without a row
+      for (int i = 0; i < P; ++i) {
+        x[k][i] = mul2(x[k][i], dup2(rstd));
+        float2 g = cg.v[k].pair(i);
         if constexpr (GATE) {
-          const float zi = cz.v[k][i], s = sigmoid_ex2(zi), zs = zi * s, gl = g[k][i];
-          z[k][i] = gl * fmaf(x[k][i], w[k][i], b[k][i]) * fmaf(zs, 1.f - s, s);
-          g[k][i] = gl * zs;
+          const float2 zi = cz.v[k].pair(i), s = sigmoid2(zi), zs = mul2(zi, s);
+          // silu'(z) = s + z s (1 - s)
+          z[k][i] = mul2(mul2(g, fma2(x[k][i], w[k][i], b[k][i])), fma2(zs, fma2(s, dup2(-1.f), dup2(1.f)), s));
+          g = mul2(g, zs);
         }
-        if (on) {  // a row that is not there has x = 0 / sqrt(eps), which eps = 0 makes a NaN
-          gw[k][i] = fmaf(g[k][i], x[k][i], gw[k][i]);
-          gb[k][i] += g[k][i];
+        if (on) {
+          gw[k][i] = fma2(g, x[k][i], gw[k][i]);
+          gb[k][i] = add2(g, gb[k][i]);
         }
-        const float u = g[k][i] * w[k][i];
-        su += u;
-        sx = fmaf(u, x[k][i], sx);
+        u[k][i] = mul2(g, w[k][i]);
+        su = add2(su, u[k][i]);
+        sx = fma2(u[k][i], x[k][i], sx);
       }
-    const float2 r = sum(su, sx);
-    if (!on) continue;
-    const float c0 = -rstd * r.x * inv_n, c1 = -rstd * r.y * inv_n;
+    const float2 r = sum(su.x + su.y, sx.x + sx.y);
+    if (on) {
+      const float2 c0 = dup2(-rstd * r.x * inv_n), c1 = dup2(-rstd * r.y * inv_n);
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int col = (k * TS + tm.lane) * V;
-      if (col >= p.N) continue;
-      float o[V];
+      for (int k = 0; k < K; ++k) {
+        if (!in[k]) continue;
+        float2 o[P];
 #pragma unroll
-      for (int i = 0; i < V; ++i) o[i] = fmaf(rstd * g[k][i], w[k][i], fmaf(c1, x[k][i], c0));
-      store_vec<T, V>(static_cast<T*>(p.gx) + off + col, o);
-      if constexpr (GATE) store_vec<T, V>(static_cast<T*>(p.ggate) + off + col, z[k]);
+        for (int i = 0; i < P; ++i) o[i] = fma2(dup2(rstd), u[k][i], fma2(c1, x[k][i], c0));
+        store_pairs_as<T, V>(gx_at + k * TS * V, o);
+        if constexpr (GATE) store_pairs_as<T, V>(gz_at + k * TS * V, z[k]);
+      }
     }
+    gx_at += stride;
+    if constexpr (GATE) gz_at += stride;
   }
   const long long slice = ((long long)blockIdx.x * (kCtaThreads<TS> / TS) + threadIdx.x / TS) / p.G;
   if (slice >= p.slices) return;
   float* part = p.part + (size_t)slice * 2 * p.G * p.N + (size_t)tm.g * p.N;
 #pragma unroll
   for (int k = 0; k < K; ++k) {
+    if (!in[k]) continue;
     const int col = (k * TS + tm.lane) * V;
-    if (col >= p.N) continue;
-    store_vec<float, V>(part + col, gw[k]);
-    store_vec<float, V>(part + (size_t)p.G * p.N + col, gb[k]);
+    store_pairs_as<float, V>(part + col, gw[k]);
+    store_pairs_as<float, V>(part + (size_t)p.G * p.N + col, gb[k]);
   }
 }
 
@@ -257,13 +305,13 @@ __device__ __forceinline__ float row_stats(const T* row, int N, float inv_n, flo
                                            TeamSum<kMaxTeam>& sum) {
   float s = 0.f;
   for (int i = threadIdx.x; i < N; i += kMaxTeam) s += IO<T>::to_f(row[i]);
-  mean = sum(s, 0.f).x * inv_n;
+  mean = sum(s) * inv_n;
   float q = 0.f;
   for (int i = threadIdx.x; i < N; i += kMaxTeam) {
     const float d = IO<T>::to_f(row[i]) - mean;
     q = fmaf(d, d, q);
   }
-  return 1.f / sqrtf(fmaf(sum(q, 0.f).x, inv_n, eps));
+  return rsqrtf(fmaf(sum(q), inv_n, eps));
 }
 
 template <typename T>
