@@ -487,7 +487,7 @@ rwkv_status rwkv_selective_scan_step(int64_t B, int64_t C, int64_t N, rwkv_dtype
   const size_t esz = bf16 ? 2 : 4;
   if (!aligned(16, {h_in, h_out}) || !aligned(esz, {x, dt, b, c, z, y}) || !aligned(4, {a_log, d, dt_bias}))
     return RWKV_ERR_UNSUPPORTED;
-  if (!grid_ok((double)B * (double)C * (double)N / 1024 + 1)) return RWKV_ERR_UNSUPPORTED;
+  if (!grid_ok((double)C * (double)N / 4 + 256) || B > INT_MAX / 2) return RWKV_ERR_UNSUPPORTED;
   ScanParams p{};
   scan_fill(p, B, 1, C, N, in);
   const int v = 16 / (int)esz;
