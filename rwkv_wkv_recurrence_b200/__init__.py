@@ -559,7 +559,7 @@ class _Launch:
     it is not the current one, the tensors that the two share are recorded on both, so that memory
     freed after the call is not handed out again too early."""
 
-    __slots__ = ("device", "raw", "stream", "outputs")
+    __slots__ = ("x", "raw", "stream", "outputs")
 
     def __init__(self, x, stream):
         import torch
@@ -569,7 +569,7 @@ class _Launch:
         index, current = x.get_device(), torch._C._cuda_getDevice()
         if index != current:
             raise ValueError(f"tensors are on {x.device}, the current device is cuda:{current}")
-        self.device = x.device
+        self.x = x
         self.raw = torch._C._cuda_getCurrentRawStream(index)
         self.stream = None  # set where the launch is not on the current stream
         if stream is not None:
@@ -578,13 +578,21 @@ class _Launch:
             if stream.cuda_stream != self.raw:
                 self.stream, self.raw, self.outputs = stream, stream.cuda_stream, []
 
+    def like(self):
+        """An output shaped and typed like x, contiguous."""
+        import torch
+
+        if self.stream is None:
+            return torch.empty_like(self.x, memory_format=torch.contiguous_format)
+        return self.empty(self.x.shape, self.x.dtype)
+
     def empty(self, shape, dtype, output=True):
         import torch
 
         if self.stream is None:
-            return torch.empty(shape, dtype=dtype, device=self.device)
+            return self.x.new_empty(shape, dtype=dtype)
         with torch.cuda.stream(self.stream):
-            t = torch.empty(shape, dtype=dtype, device=self.device)
+            t = self.x.new_empty(shape, dtype=dtype)
         if output:
             self.outputs.append(t)
         return t
@@ -625,7 +633,7 @@ def rwkv_causal_conv_forward(x, weight, bias=None, state_in=None, *, silu=False,
     _dense("state_in", state_in, (B, W - 1, C), dt, dev)
     _dense("out", out, (B, T, C), dt, dev)
     ldx = _rows("x", x, (B, T, C), dt, dev)
-    y = L.empty((B, T, C), dt) if out is None else out
+    y = L.like() if out is None else out
     st = L.empty((B, W - 1, C), dt) if return_state and W > 0 else None
     _check("rwkv_causal_conv_forward",
            _fn("rwkv_causal_conv_forward")(B, T, C, W, code, _addr(weight), _addr(bias),
@@ -652,7 +660,7 @@ def rwkv_causal_conv_backward(x, weight, gy, bias=None, state_in=None, gstate_ou
     _dense("state_in", state_in, (B, W - 1, C), dt, dev)
     _dense("gstate_out", gstate_out, (B, W - 1, C), dt, dev)
     ldx = _rows("x", x, (B, T, C), dt, dev)
-    gx = L.empty((B, T, C), dt)
+    gx = L.like()
     gw = L.empty((C, W), torch.float32)
     gb = L.empty((C,), torch.float32) if bias is not None else None
     gs = L.empty((B, W - 1, C), dt) if want_gstate_in and W > 0 else None
@@ -682,7 +690,7 @@ def rwkv_causal_conv_step(x, weight, state, bias=None, *, silu=False, state_out=
     _dense("state_out", state_out, (B, W - 1, C), dt, dev)
     _dense("out", out, (B, C), dt, dev)
     ldx = _rows("x", x, (B, C), dt, dev)
-    y = L.empty((B, C), dt) if out is None else out
+    y = L.like() if out is None else out
     so = state if state_out is None else state_out
     _check("rwkv_causal_conv_step",
            _fn("rwkv_causal_conv_step")(B, C, W, code, _addr(weight), _addr(bias), ACT_SILU if silu else ACT_NONE,
@@ -724,7 +732,7 @@ def rwkv_selective_scan_forward(x, dt, b, c, a_log, d=None, dt_bias=None, z=None
     N, args = _scan_args(x, dt, b, c, a_log, d, dt_bias, z)
     _dense("h_in", h_in, (B, C, N), torch.float32, dev)
     _dense("out", out, (B, T, C), ty, dev)
-    y = L.empty((B, T, C), ty) if out is None else out
+    y = L.like() if out is None else out
     ho = L.empty((B, C, N), torch.float32) if return_state else None
     ck = L.empty(((T + CHUNK_LEN - 1) // CHUNK_LEN, B, C, N), torch.float32) if checkpoints else None
     wsb = _fn("rwkv_selective_scan_forward_workspace_bytes")(B, T, C, N, algo)
@@ -758,9 +766,9 @@ def rwkv_selective_scan_backward(x, dt, b, c, a_log, gy, d=None, dt_bias=None, z
     _dense("ckpt", ckpt, ((T + CHUNK_LEN - 1) // CHUNK_LEN, B, C, N), f32, dev)
     _dense("h_in", h_in, (B, C, N), f32, dev)
     _dense("gh_out", gh_out, (B, C, N), f32, dev)
-    gx, gdt = L.empty((B, T, C), ty), L.empty((B, T, C), ty)
+    gx, gdt = L.like(), L.like()
     gb, gc = L.empty((B, T, N), ty), L.empty((B, T, N), ty)
-    gz = L.empty((B, T, C), ty) if z is not None else None
+    gz = L.like() if z is not None else None
     ga = L.empty((C, N), f32)
     gd = L.empty((C,), f32) if d is not None else None
     gbias = L.empty((C,), f32) if dt_bias is not None else None
@@ -790,7 +798,7 @@ def rwkv_selective_scan_step(x, dt, b, c, a_log, state, d=None, dt_bias=None, z=
     _dense("state", state, (B, C, N), torch.float32, dev)
     _dense("state_out", state_out, (B, C, N), torch.float32, dev)
     _dense("out", out, (B, C), ty, dev)
-    y = L.empty((B, C), ty) if out is None else out
+    y = L.like() if out is None else out
     so = state if state_out is None else state_out
     _check("rwkv_selective_scan_step",
            _fn("rwkv_selective_scan_step")(B, C, N, code, *args, _addr(y), _addr(state), _addr(so), L.raw))
@@ -824,7 +832,7 @@ def rwkv_layer_norm_forward(x, weight, bias=None, gate=None, *, groups=1, eps=1e
     code = _io_code("x", x)
     M, N = _norm_args(x, weight, bias, gate, groups)
     _dense("out", out, x.shape, x.dtype, x.device)
-    y = L.empty(x.shape, x.dtype) if out is None else out
+    y = L.like() if out is None else out
     _check("rwkv_layer_norm_forward",
            _fn("rwkv_layer_norm_forward")(M, groups, N, code, _addr(weight), _addr(bias), eps, _addr(x), _addr(gate),
                                           _addr(y), L.raw))
@@ -842,10 +850,10 @@ def rwkv_layer_norm_backward(x, weight, gy, bias=None, gate=None, *, groups=1, e
     M, N = _norm_args(x, weight, bias, gate, groups)
     _dense("gy", gy, x.shape, x.dtype, x.device)
     C = x.shape[-1]
-    gx = L.empty(x.shape, x.dtype)
+    gx = L.like()
     gw = L.empty((C,), torch.float32)
     gb = L.empty((C,), torch.float32) if bias is not None else None
-    gg = L.empty(x.shape, x.dtype) if gate is not None else None
+    gg = L.like() if gate is not None else None
     wsb = _fn("rwkv_layer_norm_backward_workspace_bytes")(M, groups, N, code)
     ws = L.workspace(wsb)
     _check("rwkv_layer_norm_backward",
