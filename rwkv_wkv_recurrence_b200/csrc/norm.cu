@@ -26,7 +26,11 @@ namespace rwkv {
 namespace {
 
 constexpr int kMaxTeam = 512;
-constexpr int kTargetThreads = 148 * 1536;  // threads a launch aims at (three quarters of what the SMs hold)
+// Threads a launch aims at: enough for two turns of CTAs.  Half of that for the backward's wide teams,
+// whose column sums, one set per team, are large beside the rows a team takes (fp32 8192 x 768: 18.2 +
+// 10.3 us of reduction with the full number, 19.5 + 7.0 with half; 16384 x 40 heads of 64 in bf16: 82
+// against 94 us, so narrow teams keep the full number).
+constexpr int kFillThreads = 148 * 1536;
 
 // Sums over a team, for all its threads: one value, or two.  Teams wider than a warp are whole CTAs;
 // `buf` alternates between two halves, so one barrier a call is enough.
@@ -473,10 +477,11 @@ cudaError_t run(bool bf16, bool vec, const NormParams& p, cudaStream_t st) {
   return vec ? run_v<BWD, float, 4>(p, st) : run_v<BWD, float, 1>(p, st);
 }
 
-// Slices that give about kTargetThreads threads, at least `min_rows` rows each.
-int slices_for(long long M, int G, int N, bool vec, bool bf16, int min_rows) {
+// Sets of rows (slices) that give about kFillThreads threads; 4 rows or more each in the backward.
+int slices_for(long long M, int G, int N, bool vec, bool bf16, bool bwd) {
   const int ts0 = team_shape(N / (vec ? (bf16 ? 8 : 4) : 1)).ts, ts = ts0 == 0 ? kMaxTeam : ts0;
-  const long long want = std::max<long long>(1, kTargetThreads / ((long long)ts * G));
+  const long long want = std::max<long long>(1, (bwd && ts > 32 ? kFillThreads / 2 : kFillThreads) / ((long long)ts * G));
+  const int min_rows = bwd ? 4 : 1;
   return (int)std::max<long long>(1, std::min<long long>(want, (M + min_rows - 1) / min_rows));
 }
 
@@ -484,12 +489,12 @@ int slices_for(long long M, int G, int N, bool vec, bool bf16, int min_rows) {
 
 // Depends on sizes alone (not on alignment), so that the workspace query needs no pointers.
 int norm_bwd_slices(long long M, int G, int N, bool bf16) {
-  return slices_for(M, G, N, N % (bf16 ? 8 : 4) == 0, bf16, 4);
+  return slices_for(M, G, N, N % (bf16 ? 8 : 4) == 0, bf16, true);
 }
 
 cudaError_t launch_norm_fwd(bool bf16, bool vec, const NormParams& p0, cudaStream_t st) {
   NormParams p = p0;
-  p.slices = slices_for(p.M, p.G, p.N, vec, bf16, 1);
+  p.slices = slices_for(p.M, p.G, p.N, vec, bf16, false);
   return run<false>(bf16, vec, p, st);
 }
 

@@ -83,17 +83,15 @@ struct Stage {
       }
     }
   }
-  // Elements i and i + 1 (i even).
-  __device__ __forceinline__ float2 pair(int i) const {
-    const T* p = reinterpret_cast<const T*>(raw + (i / kElems * kThreads + threadIdx.x) * kPiece) + i % kElems;
-    float f[2];
-    if constexpr (kElems >= 2) {
-      load_vec<T, 2>(p, f);
-    } else {
-      f[0] = IO<T>::to_f(p[0]);
-      f[1] = IO<T>::to_f(*reinterpret_cast<const T*>(raw + ((i + 1) * kThreads + threadIdx.x) * kPiece));
+  // Back into registers: the run's elements, as loaded.
+  __device__ __forceinline__ void read(Raw<T, RUN>& r) const {
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k) {
+      Raw<T, kElems> q;
+      q.load(reinterpret_cast<const T*>(raw + (k * kThreads + threadIdx.x) * kPiece));
+#pragma unroll
+      for (int i = 0; i < kPiece / 4; ++i) r.w[k * (kPiece / 4) + i] = q.w[i];
     }
-    return make_float2(f[0], f[1]);
   }
 };
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -103,8 +101,9 @@ template <typename T, int N>
 struct __align__(16) Smem {
   using S = Shape<N>;
   float4 dxg[kTile][S::kCh];              // (Δ, Δ x, g, x), then (gx, gdt / σ, p, -); columns permuted
-  float bc[2][kTile][4][N];               // B and C: copy p holds state 4 s + i at 4 s + (i ^ p)
+  float bc[2][kTile][4 * N + 16];         // B and C: copy p (at p N) holds state 4 s + i at 4 s + (i ^ p)
   float red[kWarps][kTile][2 * N];        // per warp: gC, gB of a token
+  float bias[S::kCh];                     // dt_bias
   float2 sg[S::kRun][kThreads];           // σ(dt + bias), gy silu'(z): each thread's own
   float4 snap[kTile / kSub][2][kThreads]; // states before tokens 0, 4, 8, 12, each thread's own
   Stage<T, S::kRun> x, dt, z, gy;
@@ -185,16 +184,23 @@ __global__ void __launch_bounds__(kThreads, 3) scan_bwd_kernel(const __grid_cons
 #pragma unroll
   for (int i = 0; i < RUN; ++i) gd[i] = gbias[i] = 0.f;
 
+  for (int i = tid; i < CH; i += kThreads)
+    sm.bias[i] = f.dt_bias != nullptr && ct * CH + i < f.C ? f.dt_bias[ct * CH + i] : 0.f;
+  __syncthreads();
+
   constexpr int QT = (S::kQuads + kThreads - 1) / kThreads;
   Raw<T, 4> bc[QT];
+  const size_t row0 = (size_t)bb * f.T + lt;
+  const T* x_at = static_cast<const T*>(f.x) + row0 * f.ldx + c0;
+  const T* dt_at = static_cast<const T*>(f.dt) + row0 * f.lddt + c0;
+  const T* gy_at = static_cast<const T*>(p.gy) + row0 * f.C + c0;
+  const T* z_at = f.z != nullptr ? static_cast<const T*>(f.z) + row0 * f.ldz + c0 : nullptr;
   const auto fetch = [&](int ts) {  // a tile's inputs, on their way
-    const bool ok = ts + lt < t1;
-    const size_t row = (size_t)bb * f.T + (ok ? ts + lt : 0);
-    const int n = ok ? nc : 0;
-    sm.x.fetch(static_cast<const T*>(f.x) + row * f.ldx + c0, n, f.vec);
-    sm.dt.fetch(static_cast<const T*>(f.dt) + row * f.lddt + c0, n, f.vec);
-    sm.gy.fetch(static_cast<const T*>(p.gy) + row * f.C + c0, n, f.vec);
-    if (f.z != nullptr) sm.z.fetch(static_cast<const T*>(f.z) + row * f.ldz + c0, n, f.vec);
+    const int n = ts + lt < t1 ? nc : 0;  // n = 0: zeros, nothing read
+    sm.x.fetch(x_at + (ptrdiff_t)ts * f.ldx, n, f.vec);
+    sm.dt.fetch(dt_at + (ptrdiff_t)ts * f.lddt, n, f.vec);
+    sm.gy.fetch(gy_at + (ptrdiff_t)ts * f.C, n, f.vec);
+    if (f.z != nullptr) sm.z.fetch(z_at + (ptrdiff_t)ts * f.ldz, n, f.vec);
     cp_async_commit();
 #pragma unroll
     for (int k = 0; k < QT; ++k) {
@@ -227,39 +233,44 @@ __global__ void __launch_bounds__(kThreads, 3) scan_bwd_kernel(const __grid_cons
   for (; ts >= t0; ts -= kTile) {
     const bool tact = ts + lt < t1;
     cp_async_wait_all();
+    {
+      Raw<T, RUN> rx, rdt, rg, rz;
+      sm.x.read(rx);
+      sm.dt.read(rdt);
+      sm.gy.read(rg);
+      if (f.z != nullptr) sm.z.read(rz);
 #pragma unroll
-    for (int i = 0; i < RUN; i += 2) {
-      float2 v = sm.dt.pair(i), g = sm.gy.pair(i), e;
-      const float2 x = sm.x.pair(i);
-      if (f.dt_bias != nullptr) {
-        if (i < nc) v.x += f.dt_bias[c0 + i];
-        if (i + 1 < nc) v.y += f.dt_bias[c0 + i + 1];
+      for (int i = 0; i < RUN; i += 2) {
+        const int cc = lq * RUN + i;
+        float2 g = rg.pair(i / 2), e;
+        const float2 x = rx.pair(i / 2);
+        const float2 v = add2(rdt.pair(i / 2), *reinterpret_cast<const float2*>(&sm.bias[cc]));
+        float2 dl = softplus2(v, e);
+        const float2 d1 = add2(e, dup2(1.f)), r1 = make_float2(rcp_approx(d1.x), rcp_approx(d1.y)), er = mul2(e, r1);
+        const float2 sig = make_float2(v.x >= 0.f ? r1.x : er.x, v.y >= 0.f ? r1.y : er.y);
+        float2 gpre = dup2(0.f);  // gy silu'(z) = gy (s + z s (1 - s))
+        if (f.z != nullptr) {
+          const float2 z = rz.pair(i / 2), s = sigmoid2(z), zs = mul2(z, s);
+          gpre = mul2(g, fma2(zs, fma2(s, dup2(-1.f), dup2(1.f)), s));
+          g = mul2(g, zs);
+        }
+        // behind the end and past the last channel x = gy = 0 were fetched; Δ = 0 keeps the state
+        if (!tact || i >= nc) dl.x = 0.f;
+        if (!tact || i + 1 >= nc) dl.y = 0.f;
+        const float2 dx = mul2(dl, x), gxx = fma2(g, x, make_float2(gd[i], gd[i + 1]));
+        gd[i] = gxx.x, gd[i + 1] = gxx.y;
+        sm.dxg[lt][S::col(cc)] = make_float4(dl.x, dx.x, g.x, x.x);
+        sm.dxg[lt][S::col(cc + 1)] = make_float4(dl.y, dx.y, g.y, x.y);
+        sm.sg[i][tid] = make_float2(sig.x, gpre.x);
+        sm.sg[i + 1][tid] = make_float2(sig.y, gpre.y);
       }
-      const float2 dl = softplus2(v, e);
-      const float rx = rcp_approx(1.f + e.x), ry = rcp_approx(1.f + e.y);
-      float2 sig = make_float2(v.x >= 0.f ? rx : e.x * rx, v.y >= 0.f ? ry : e.y * ry);
-      float2 gpre = dup2(0.f);  // gy silu'(z)
-      if (f.z != nullptr) {
-        const float2 z = sm.z.pair(i);
-        const float sx = sigmoid_ex2(z.x), sy = sigmoid_ex2(z.y);
-        gpre = make_float2(g.x * sx * fmaf(z.x, 1.f - sx, 1.f), g.y * sy * fmaf(z.y, 1.f - sy, 1.f));
-        g = make_float2(g.x * (z.x * sx), g.y * (z.y * sy));
-      }
-      const bool on0 = tact && i < nc, on1 = tact && i + 1 < nc;
-      const int cc = lq * RUN + i;
-      sm.dxg[lt][S::col(cc)] = on0 ? make_float4(dl.x, dl.x * x.x, g.x, x.x) : make_float4(0.f, 0.f, 0.f, 0.f);
-      sm.dxg[lt][S::col(cc + 1)] = on1 ? make_float4(dl.y, dl.y * x.y, g.y, x.y) : make_float4(0.f, 0.f, 0.f, 0.f);
-      sm.sg[i][tid] = make_float2(sig.x, gpre.x);
-      sm.sg[i + 1][tid] = make_float2(sig.y, gpre.y);
-      if (on0) gd[i] = fmaf(g.x, x.x, gd[i]);
-      if (on1) gd[i + 1] = fmaf(g.y, x.y, gd[i + 1]);
     }
 #pragma unroll
     for (int k = 0; k < QT; ++k) {
       const int id = tid + k * kThreads;
       if (S::kQuads % kThreads != 0 && id >= S::kQuads) continue;
       const int which = id >= S::kQuads / 2, qi = which ? id - S::kQuads / 2 : id;
-      float* dst = &sm.bc[which][qi / (N / 4)][0][qi % (N / 4) * 4];
+      float* dst = &sm.bc[which][qi / (N / 4)][qi % (N / 4) * 4];
       const float a = bc[k][0], b = bc[k][1], c = bc[k][2], d = bc[k][3];
       *reinterpret_cast<float4*>(dst) = make_float4(a, b, c, d);
       *reinterpret_cast<float4*>(dst + N) = make_float4(b, a, d, c);
@@ -285,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 3) scan_bwd_kernel(const __grid_cons
         if (k == kTile - kSub) break;
       }
       float2 bv[2];
-      load_pairs<2>(&sm.bc[0][k][ord][sub * kSN], bv);
+      load_pairs<2>(&sm.bc[0][k][ord * N + sub * kSN], bv);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const float2 d = *reinterpret_cast<const float2*>(&sm.dxg[k][col[j]]);
@@ -304,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 3) scan_bwd_kernel(const __grid_cons
 #pragma unroll
       for (int k = 0; k < kSub; ++k) {
         float2 bv[2];
-        load_pairs<2>(&sm.bc[0][k0 + k][ord][sub * kSN], bv);
+        load_pairs<2>(&sm.bc[0][k0 + k][ord * N + sub * kSN], bv);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const float2 d = *reinterpret_cast<const float2*>(&sm.dxg[k0 + k][col[j]]);
@@ -319,8 +330,8 @@ __global__ void __launch_bounds__(kThreads, 3) scan_bwd_kernel(const __grid_cons
 #pragma unroll
       for (int k = kSub - 1; k >= 0; --k) {
         float2 bv[2], cv[2], vc[2], vb[2];  // vc, vb: this thread's part of gC and gB
-        load_pairs<2>(&sm.bc[0][k0 + k][ord][sub * kSN], bv);
-        load_pairs<2>(&sm.bc[1][k0 + k][ord][sub * kSN], cv);
+        load_pairs<2>(&sm.bc[0][k0 + k][ord * N + sub * kSN], bv);
+        load_pairs<2>(&sm.bc[1][k0 + k][ord * N + sub * kSN], cv);
         float tp[2], t1s[2], t2[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
@@ -397,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 3) scan_bwd_kernel(const __grid_cons
         const float2 sg = sm.sg[i][tid];
         ox[i] = d.x;
         odt[i] = sg.x * d.y;
-        if (i < nc) gbias[i] += odt[i];
+        gbias[i] += odt[i];  // 0 for a token or channel that is not there
         oz[i] = sg.y * d.z;
       }
       const size_t off = ((size_t)bb * f.T + ts + lt) * f.C + c0;
