@@ -508,7 +508,7 @@ static rwkv_status norm_check(int64_t M, int64_t G, int64_t N, rwkv_dtype dtype,
 
 size_t rwkv_layer_norm_backward_workspace_bytes(int64_t M, int64_t G, int64_t N, rwkv_dtype dtype) {
   if (M <= 0 || G <= 0 || N <= 0 || !fits_int(G) || !fits_int(N) || !dtype_ok(dtype) || G * N > INT_MAX / 2) return 0;
-  return (size_t)norm_bwd_slices(M, (int)G, (int)N, dtype == RWKV_BF16) * 2 * G * N * sizeof(float);
+  return (size_t)norm_bwd_parts(M, (int)G, (int)N, dtype == RWKV_BF16) * 2 * G * N * sizeof(float);
 }
 
 rwkv_status rwkv_layer_norm_forward(int64_t M, int64_t G, int64_t N, rwkv_dtype dtype, const float* weight,

@@ -25,7 +25,8 @@ constexpr int kFwdStretch = 32;  // tokens per thread, forward
 constexpr int kBwdStretch = 64;  // tokens per thread, backward
 constexpr int kBwdWarps = 8;     // stretches per CTA (their weight-gradient sums meet in shared memory)
 constexpr int kStepStreams = 2;  // streams per thread, step
-constexpr int kAhead = 8;        // tokens fetched together
+constexpr int kAhead = 8;        // tokens fetched together, forward
+constexpr int kBwdAhead = 8;     // tokens fetched together, backward
 
 // Channels are worked on in pairs (packed arithmetic); with V = 1 a pair's second half is idle.
 template <int V>
@@ -182,17 +183,17 @@ __global__ void __launch_bounds__(32 * kBwdWarps) conv_bwd_kernel(const __grid_c
     const T* xr = static_cast<const T*>(p.x) + ((size_t)b * p.T + t0) * p.ldx + c;
     const T* gr = static_cast<const T*>(p.gy) + ((size_t)b * p.T + t0) * p.C + c;
     T* gxr = static_cast<T*>(p.gx) + ((size_t)b * p.T + t0) * p.C + c;  // of the token being fetched for
-    Raw<T, V> nx[kAhead], ng[kAhead];
-    const auto fetch = [&](int t) {  // tokens t .. t + kAhead - 1, xr and gr pointing at the first
-      if (t + kAhead <= p.T) {
+    Raw<T, V> nx[kBwdAhead], ng[kBwdAhead];
+    const auto fetch = [&](int t) {  // tokens t .. t + kBwdAhead - 1, xr and gr pointing at the first
+      if (t + kBwdAhead <= p.T) {
 #pragma unroll
-        for (int a = 0; a < kAhead; ++a) {
+        for (int a = 0; a < kBwdAhead; ++a) {
           nx[a].load(xr + (size_t)a * p.ldx);
           ng[a].load(gr + (size_t)a * p.C);
         }
       } else {
 #pragma unroll
-        for (int a = 0; a < kAhead; ++a)
+        for (int a = 0; a < kBwdAhead; ++a)
           if (t + a < p.T) {
             nx[a].load(xr + (size_t)a * p.ldx);
             ng[a].load(gr + (size_t)a * p.C);
@@ -238,17 +239,17 @@ __global__ void __launch_bounds__(32 * kBwdWarps) conv_bwd_kernel(const __grid_c
 #pragma unroll
         for (int j = 0; j < W; ++j) e[i] = fma2(w[j][i], gp[W - 1 - j][i], e[i]);
     };
-    for (int t = t0; t < tend; t += kAhead) {
-      Raw<T, V> cx[kAhead], cg_[kAhead];
+    for (int t = t0; t < tend; t += kBwdAhead) {
+      Raw<T, V> cx[kBwdAhead], cg_[kBwdAhead];
 #pragma unroll
-      for (int a = 0; a < kAhead; ++a) cx[a] = nx[a], cg_[a] = ng[a];
-      xr += (size_t)kAhead * p.ldx;
-      gr += (size_t)kAhead * p.C;
-      if (t + kAhead < tend) fetch(t + kAhead);
-      if (t - (W - 1) >= t0 && t + kAhead <= t1) {
+      for (int a = 0; a < kBwdAhead; ++a) cx[a] = nx[a], cg_[a] = ng[a];
+      xr += (size_t)kBwdAhead * p.ldx;
+      gr += (size_t)kBwdAhead * p.C;
+      if (t + kBwdAhead < tend) fetch(t + kBwdAhead);
+      if (t - (W - 1) >= t0 && t + kBwdAhead <= t1) {
         // all tokens owned, none before the stretch
 #pragma unroll
-        for (int a = 0; a < kAhead; ++a) {
+        for (int a = 0; a < kBwdAhead; ++a) {
           grad(cx[a], cg_[a], true);
           float2 o[P];
 #pragma unroll
@@ -258,7 +259,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps) conv_bwd_kernel(const __grid_c
         }
       } else {
 #pragma unroll
-        for (int a = 0; a < kAhead; ++a) {
+        for (int a = 0; a < kBwdAhead; ++a) {
           const int ta = t + a;
           if (ta >= tend) break;
           if (ta < p.T) {
@@ -289,7 +290,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps) conv_bwd_kernel(const __grid_c
           }
         }
       }
-      gxr += (size_t)kAhead * p.C;
+      gxr += (size_t)kBwdAhead * p.C;
     }
   }
 #pragma unroll

@@ -308,10 +308,10 @@ struct NormParams {
   void* ggate;
   float* gweight;       // [G,N]
   float* gbias;         // [G,N] or null
-  float* part;          // [slices][2][G,N] workspace
+  float* part;          // [norm_bwd_parts()][2][G,N] workspace
   int slices;           // sets of rows whose weight gradients are summed apart
 };
-int norm_bwd_slices(long long M, int G, int N, bool bf16);
+int norm_bwd_parts(long long M, int G, int N, bool bf16);
 cudaError_t launch_norm_fwd(bool bf16, bool vec, const NormParams& p, cudaStream_t st);
 cudaError_t launch_norm_bwd(bool bf16, bool vec, const NormParams& p, cudaStream_t st);
 

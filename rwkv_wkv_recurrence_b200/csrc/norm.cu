@@ -32,10 +32,17 @@ constexpr int kMaxTeam = 512;
 // against 94 us, so narrow teams keep the full number).
 constexpr int kFillThreads = 148 * 1536;
 
-// Sums over a team, for all its threads: one value, or two.  Teams wider than a warp are whole CTAs;
-// `buf` alternates between two halves, so one barrier a call is enough.
+template <int TS>
+constexpr int kCtaThreads = TS > 256 ? TS : 256;
+template <int TS>
+constexpr int kTeams = kCtaThreads<TS> / TS;  // teams per CTA
+
+// Sums over a team, for all its threads: one value, or two.  Teams wider than a warp meet at their own
+// barrier; `buf` alternates between two halves, so one barrier a call is enough.
 template <int TS>
 struct TeamSum {
+  static constexpr int kWarps = TS > 32 ? TS / 32 : 1;
+  static constexpr int kBuf = 2 * kWarps * kTeams<TS>;
   float2* buf;
   int phase = 0;
   template <bool TWO>
@@ -47,14 +54,17 @@ struct TeamSum {
       if (TWO) b += __shfl_xor_sync(0xffffffffu, b, o);
     }
     if constexpr (TS > 32) {
-      constexpr int NW = TS / 32;
-      float2* s = buf + phase * NW;
+      const int team = threadIdx.x / TS;
+      float2* s = buf + (team * 2 + phase) * kWarps;
       phase ^= 1;
-      if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = make_float2(a, b);
-      __syncthreads();
+      if ((threadIdx.x & 31) == 0) s[threadIdx.x % TS / 32] = make_float2(a, b);
+      if constexpr (kTeams<TS> == 1)
+        __syncthreads();
+      else
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "n"(TS) : "memory");
       a = b = 0.f;
 #pragma unroll
-      for (int i = 0; i < NW; ++i) {
+      for (int i = 0; i < kWarps; ++i) {
         a += s[i].x;
         if (TWO) b += s[i].y;
       }
@@ -65,18 +75,14 @@ struct TeamSum {
   __device__ __forceinline__ float2 operator()(float a, float b) { return run<true>(a, b); }
 };
 
-template <int TS>
-constexpr int kCtaThreads = TS > 32 ? TS : 256;
-
 // Where a team works: its group, first row, row stride.
 template <int TS>
 struct Team {
   int lane, g;
   long long m, step, turns;
   __device__ __forceinline__ explicit Team(const NormParams& p) {
-    constexpr int PER = kCtaThreads<TS> / TS;
     lane = threadIdx.x % TS;
-    const long long id = (long long)blockIdx.x * PER + threadIdx.x / TS;
+    const long long id = (long long)blockIdx.x * kTeams<TS> + threadIdx.x / TS;
     g = (int)(id % p.G);
     m = id / p.G;
     step = p.slices;
@@ -146,7 +152,7 @@ __device__ __forceinline__ float center(const RowPart<T, V, K, TS>& r, float2 (&
 template <typename T, int V, int K, int TS, bool GATE>
 __global__ void __launch_bounds__(kCtaThreads<TS>) norm_fwd_kernel(const __grid_constant__ NormParams p) {
   constexpr int P = (V + 1) / 2;
-  __shared__ float2 buf[2 * kMaxTeam / 32];
+  __shared__ float2 buf[TeamSum<TS>::kBuf];
   TeamSum<TS> sum{buf};
   const Team<TS> tm(p);
   const float inv_n = 1.f / (float)p.N;
@@ -206,7 +212,7 @@ __global__ void __launch_bounds__(kCtaThreads<TS>) norm_fwd_kernel(const __grid_
 template <typename T, int V, int K, int TS, bool GATE>
 __global__ void __launch_bounds__(kCtaThreads<TS>) norm_bwd_kernel(const __grid_constant__ NormParams p) {
   constexpr int P = (V + 1) / 2;
-  __shared__ float2 buf[2 * kMaxTeam / 32];
+  __shared__ float2 buf[TeamSum<TS>::kBuf];
   TeamSum<TS> sum{buf};
   const Team<TS> tm(p);
   const float inv_n = 1.f / (float)p.N;
@@ -291,9 +297,34 @@ __global__ void __launch_bounds__(kCtaThreads<TS>) norm_bwd_kernel(const __grid_
     gx_at += stride;
     if constexpr (GATE) gz_at += stride;
   }
-  const long long slice = ((long long)blockIdx.x * (kCtaThreads<TS> / TS) + threadIdx.x / TS) / p.G;
-  if (slice >= p.slices) return;
-  float* part = p.part + (size_t)slice * 2 * p.G * p.N + (size_t)tm.g * p.N;
+  // With one group a CTA's teams hold the same columns and add up in shared memory, in order; else
+  // each writes its own.
+  long long part_id = ((long long)blockIdx.x * kTeams<TS> + threadIdx.x / TS) / p.G;
+  bool write = part_id < p.slices;
+  if constexpr (kTeams<TS> > 1) {
+    __shared__ float2 acc[2][K * TS * P];
+    if (p.G == 1) {
+      const int team = threadIdx.x / TS;
+      for (int t = 0; t < kTeams<TS>; ++t) {
+        if (team == t) {
+#pragma unroll
+          for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+              float2& a = acc[0][(k * P + i) * TS + tm.lane];
+              float2& c = acc[1][(k * P + i) * TS + tm.lane];
+              if (t > 0) gw[k][i] = add2(a, gw[k][i]), gb[k][i] = add2(c, gb[k][i]);
+              a = gw[k][i], c = gb[k][i];
+            }
+        }
+        __syncthreads();
+      }
+      part_id = blockIdx.x;
+      write = team == kTeams<TS> - 1;  // holds the sum of all
+    }
+  }
+  if (!write) return;
+  float* part = p.part + (size_t)part_id * 2 * p.G * p.N + (size_t)tm.g * p.N;
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     if (!in[k]) continue;
@@ -320,7 +351,7 @@ __device__ __forceinline__ float row_stats(const T* row, int N, float inv_n, flo
 
 template <typename T>
 __global__ void __launch_bounds__(kMaxTeam) norm_fwd_wide_kernel(const NormParams p) {
-  __shared__ float2 buf[2 * kMaxTeam / 32];
+  __shared__ float2 buf[TeamSum<kMaxTeam>::kBuf];
   TeamSum<kMaxTeam> sum{buf};
   Team<kMaxTeam> tm(p);
   for (long long m = tm.m; m < p.M; m += tm.step) {
@@ -342,7 +373,7 @@ __global__ void __launch_bounds__(kMaxTeam) norm_fwd_wide_kernel(const NormParam
 
 template <typename T>
 __global__ void __launch_bounds__(kMaxTeam) norm_bwd_wide_kernel(const NormParams p) {
-  __shared__ float2 buf[2 * kMaxTeam / 32];
+  __shared__ float2 buf[TeamSum<kMaxTeam>::kBuf];
   TeamSum<kMaxTeam> sum{buf};
   Team<kMaxTeam> tm(p);
   const float inv_n = 1.f / (float)p.N;
@@ -431,7 +462,8 @@ TeamShape team_shape(int nv) {
   if (nv <= 16) return {16, 1};
   if (nv <= 32) return {32, 1};
   if (nv <= 64) return {32, 2};
-  if (nv <= 128) return {128, 1};
+  if (nv <= 128) return {64, 2};
+  if (nv <= 192) return {64, 3};
   if (nv <= 256) return {128, 2};
   if (nv <= 512) return {512, 1};
   if (nv <= 1024) return {512, 2};
@@ -440,9 +472,8 @@ TeamShape team_shape(int nv) {
 
 template <bool BWD, typename T, int V, int K, int TS>
 cudaError_t run_team(const NormParams& p, cudaStream_t st) {
-  constexpr int PER = kCtaThreads<TS> / TS;
   const long long teams = (long long)p.slices * p.G;
-  const unsigned grid = (unsigned)((teams + PER - 1) / PER);
+  const unsigned grid = (unsigned)((teams + kTeams<TS> - 1) / kTeams<TS>);
   const auto kernel =
       BWD ? (p.gate != nullptr ? norm_bwd_kernel<T, V, K, TS, true> : norm_bwd_kernel<T, V, K, TS, false>)
           : (p.gate != nullptr ? norm_fwd_kernel<T, V, K, TS, true> : norm_fwd_kernel<T, V, K, TS, false>);
@@ -458,7 +489,8 @@ cudaError_t run_v(const NormParams& p, cudaStream_t st) {
     case 16 * 4 + 1: return run_team<BWD, T, V, 1, 16>(p, st);
     case 32 * 4 + 1: return run_team<BWD, T, V, 1, 32>(p, st);
     case 32 * 4 + 2: return run_team<BWD, T, V, 2, 32>(p, st);
-    case 128 * 4 + 1: return run_team<BWD, T, V, 1, 128>(p, st);
+    case 64 * 4 + 2: return run_team<BWD, T, V, 2, 64>(p, st);
+    case 64 * 4 + 3: return run_team<BWD, T, V, 3, 64>(p, st);
     case 128 * 4 + 2: return run_team<BWD, T, V, 2, 128>(p, st);
     case 512 * 4 + 1: return run_team<BWD, T, V, 1, 512>(p, st);
     case 512 * 4 + 2: return run_team<BWD, T, V, 2, 512>(p, st);
@@ -487,9 +519,22 @@ int slices_for(long long M, int G, int N, bool vec, bool bf16, bool bwd) {
 
 }  // namespace
 
-// Depends on sizes alone (not on alignment), so that the workspace query needs no pointers.
-int norm_bwd_slices(long long M, int G, int N, bool bf16) {
-  return slices_for(M, G, N, N % (bf16 ? 8 : 4) == 0, bf16, true);
+namespace {
+// Sets of column sums that the backward's teams write: a CTA's teams share one where there is one group.
+int parts_for(int slices, int G, int nv) {
+  const int ts = team_shape(nv).ts;
+  const int teams = ts == 0 ? 1 : (ts > 256 ? 1 : 256 / ts);
+  return G == 1 ? (slices + teams - 1) / teams : slices;
+}
+}  // namespace
+
+// Bounds the sets of column sums by sizes alone (aligned or not), so that the workspace query needs no
+// pointers.
+int norm_bwd_parts(long long M, int G, int N, bool bf16) {
+  const int v = bf16 ? 8 : 4;
+  int n = parts_for(slices_for(M, G, N, false, bf16, true), G, N);
+  if (N % v == 0) n = std::max(n, parts_for(slices_for(M, G, N, true, bf16, true), G, N / v));
+  return n;
 }
 
 cudaError_t launch_norm_fwd(bool bf16, bool vec, const NormParams& p0, cudaStream_t st) {
@@ -500,11 +545,12 @@ cudaError_t launch_norm_fwd(bool bf16, bool vec, const NormParams& p0, cudaStrea
 
 cudaError_t launch_norm_bwd(bool bf16, bool vec, const NormParams& p0, cudaStream_t st) {
   NormParams p = p0;
-  p.slices = norm_bwd_slices(p.M, p.G, p.N, bf16);
+  p.slices = slices_for(p.M, p.G, p.N, vec, bf16, true);
   const cudaError_t e = run<true>(bf16, vec, p, st);
   if (e != cudaSuccess) return e;
   const int C = p.G * p.N;
-  norm_reduce_kernel<<<(unsigned)((2LL * C + 31) / 32), 1024, 0, st>>>(p.slices, C, p.part, p.gweight, p.gbias);
+  norm_reduce_kernel<<<(unsigned)((2LL * C + 31) / 32), 1024, 0, st>>>(
+      parts_for(p.slices, p.G, vec ? p.N / (bf16 ? 8 : 4) : p.N), C, p.part, p.gweight, p.gbias);
   return cudaGetLastError();
 }
 

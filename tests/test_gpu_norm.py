@@ -26,11 +26,11 @@ def _run(q, groups, gate, bias, eps=1e-5):
     return dict(y=y, gx=gx, gw=gw, gbias=gb, ggate=gg)
 
 
-# (rows, groups, columns): every team shape (8, 16, 32, 128 and 512 threads, one and two vectors) in wide and
+# (rows, groups, columns): every team shape (8 to 512 threads, one to three vectors) in wide and
 # in single accesses, the wide kernel, rows that do and do not fill a launch, one column
 SHAPES = [(1, 1, 1), (3, 1, 5), (5, 40, 64), (70, 3, 64), (9, 2, 77), (4, 1, 96), (33, 2, 128), (7, 1, 200),
           (5, 3, 256), (2, 1, 520), (6, 1, 768), (3, 1, 1000), (2, 2, 1001), (2, 1, 2048), (3, 1, 4096),
-          (2, 1, 8192), (2, 1, 8200), (1, 1, 2500)]
+          (2, 1, 8192), (2, 1, 8200), (1, 1, 2500), (5, 2, 1400), (40, 1, 300)]
 
 
 @DT
@@ -45,7 +45,7 @@ def test_forward_backward(cuda_device, shape, dtype):
 
 
 @DT
-@pytest.mark.parametrize("shape", [(20000, 1, 64), (3000, 40, 64), (5000, 1, 768)], ids=str)
+@pytest.mark.parametrize("shape", [(20000, 1, 64), (3000, 40, 64), (5000, 1, 768), (3001, 1, 512)], ids=str)
 def test_many_rows(cuda_device, shape, dtype):
     # teams take several rows each
     M, G, N = shape
