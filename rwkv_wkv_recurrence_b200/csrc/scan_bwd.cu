@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(kThreads, 3) scan_bwd_kernel(const __grid_cons
           load_pairs<2>(p.seg_g + (size_t)s * plane + hoff[j], x);
           const float2 sd = dup2(p.seg_dt[((size_t)s * f.B + bb) * f.C + c]);
 #pragma unroll
-          for (int q = 0; q < 2; ++q) gh[j][q] = fma2(ex2_2(mul2(sd, a2[j][q])), gh[j][q], x[q]);
+          for (int q = 0; q < 2; ++q) gh[j][q] = fma2(decay2(sd, a2[j][q]), gh[j][q], x[q]);
         }
       } else if (p.gh_out != nullptr) {
         // a copy when segmented: gh_in may be the same array, and another CTA writes it
@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, 3) scan_bwd_kernel(const __grid_cons
         const float2 d = *reinterpret_cast<const float2*>(&sm.dxg[k][col[j]]);
 #pragma unroll
         for (int q = 0; q < 2; ++q)
-          h[j][q] = fma2(ex2_2(mul2(dup2(d.x), a2[j][q])), h[j][q], mul2(dup2(d.y), bv[q]));
+          h[j][q] = fma2(decay2(dup2(d.x), a2[j][q]), h[j][q], mul2(dup2(d.y), bv[q]));
       }
     }
 
@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 3) scan_bwd_kernel(const __grid_cons
           const float2 d = *reinterpret_cast<const float2*>(&sm.dxg[k0 + k][col[j]]);
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
-            e[k][j][q] = ex2_2(mul2(dup2(d.x), a2[j][q]));
+            e[k][j][q] = decay2(dup2(d.x), a2[j][q]);
             hh[k + 1][j][q] = fma2(e[k][j][q], hh[k][j][q], mul2(dup2(d.y), bv[q]));
           }
         }

@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(Shape<N, CH_>::kThreads) scan_fwd_kernel(const
         load_pairs<2>(p.seg_h + (size_t)s * plane + hoff, x);
         const float2 sd = dup2(p.seg_dt[((size_t)s * p.B + bb) * p.C + c]);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) h[i] = fma2(ex2_2(mul2(sd, a2[i])), h[i], x[i]);
+        for (int i = 0; i < 2; ++i) h[i] = fma2(decay2(sd, a2[i]), h[i], x[i]);
       }
     } else if (seg == (REV ? p.nseg - 1 : 0) && p.h_in != nullptr) {
       // with segments the first launch keeps a copy of h_in, which the second reads: h_out may be
@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(Shape<N, CH_>::kThreads) scan_fwd_kernel(const
           const float2 d2 = dup2(q.dx[k].x), in2 = dup2(q.dx[k].y);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const float2 e = ex2_2(mul2(d2, a2[i]));
+            const float2 e = decay2(d2, a2[i]);
             h[i] = REV ? mul2(e, fma2(in2, q.b[k][i], h[i])) : fma2(e, h[i], mul2(in2, q.b[k][i]));
           }
           if constexpr (OUT) {

@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(kThreads) scan_step_kernel(const __grid_consta
       float2 h[2], acc = dup2(0.f);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        h[i] = fma2(ex2_2(mul2(dl, a2[i])), cur.h[k].pair(i), mul2(dx, cur.b[k].pair(i)));
+        h[i] = fma2(decay2(dl, a2[i]), cur.h[k].pair(i), mul2(dx, cur.b[k].pair(i)));
         acc = fma2(cur.c[k].pair(i), h[i], acc);
       }
       float y = acc.x + acc.y;
