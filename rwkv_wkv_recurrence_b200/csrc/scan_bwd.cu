@@ -159,6 +159,7 @@ __global__ void __launch_bounds__(kThreads, 3) scan_bwd_kernel(const __grid_cons
     if (cact[j]) {
       if (seg < f.nseg - 1) {  // the last segment's own gradient starts from gh_out
         load_pairs<2>(p.seg_g + (size_t)(f.nseg - 1) * plane + hoff[j], gh[j]);
+#pragma unroll 4
         for (int s = f.nseg - 2; s > seg; --s) {
           float2 x[2];
           load_pairs<2>(p.seg_g + (size_t)s * plane + hoff[j], x);

@@ -157,6 +157,7 @@ __global__ void __launch_bounds__(Shape<N, CH_>::kThreads) scan_fwd_kernel(const
   if (cact) {
     if (OUT && seg > 0) {
       load_pairs<2>(p.seg_h + hoff, h);  // segment 0's summary starts from h_in
+#pragma unroll 4
       for (int s = 1; s < seg; ++s) {
         float2 x[2];
         load_pairs<2>(p.seg_h + (size_t)s * plane + hoff, x);

@@ -79,6 +79,45 @@ def test_parts_of_wider_tensors(cuda_device, shape, dtype):
     ref.check_all(_backward(q, ck), r)
 
 
+@pytest.mark.parametrize("at", [1, 3])
+def test_b_and_c_off_the_16_byte_grid(cuda_device, at):
+    # b and c as parts of rows at an odd place (single accesses) beside x, dt, z in wide ones
+    p, v = ref.scan_inputs(2, 40, 48, 16, seed=36, dtype=torch.bfloat16)
+    r = ref.scan(**p)
+    q = _dev(p, v, cuda_device)
+    rows = torch.zeros(2, 40, 48, dtype=torch.bfloat16, device=cuda_device)
+    rows[..., at: at + 16], rows[..., 24 + at: 40 + at] = q["b"], q["c"]
+    q["b"], q["c"] = rows[..., at: at + 16], rows[..., 24 + at: 40 + at]
+    y, h, ck = _forward(q, return_state=True, checkpoints=True)
+    ref.check_all(dict(y=y, h=h), r)
+    ref.check_all(_backward(q, ck), r)
+
+
+def test_step_of_many_streams(cuda_device):
+    # more streams than the grid's second dimension holds; rows of every part against single-stream calls
+    B, C, N = 70001, 4, 8
+    p, v = ref.scan_inputs(B, 1, C, N, seed=37, grads=False)
+    q = {k: (t[:, 0] if t.dim() == 3 and k != "h_in" else t) for k, t in _dev(p, v, cuda_device).items()}
+    so = torch.empty_like(q["h_in"])
+    y = rw.rwkv_selective_scan_step(*(q[k] for k in INPUTS[:5]), q["h_in"], q["d"], q["dt_bias"], q["z"], state_out=so)
+    for b in (0, 1, 2, 65534, 65535, 65536, 70000):
+        one = {k: (t[b: b + 1].contiguous() if k in ("x", "dt", "b", "c", "z", "h_in") else t) for k, t in q.items()}
+        s1 = torch.empty_like(one["h_in"])
+        y1 = rw.rwkv_selective_scan_step(*(one[k] for k in INPUTS[:5]), one["h_in"], one["d"], one["dt_bias"], one["z"],
+                                         state_out=s1)
+        assert torch.equal(y[b], y1[0]) and torch.equal(so[b], s1[0]), b
+
+
+def test_many_segments(cuda_device):
+    # one channel tile over a long sequence: as many segments as there are tiles, folded in order
+    p, v = ref.scan_inputs(1, 1500, 5, 8, seed=38)
+    r = ref.scan(**p)
+    q = _dev(p, v, cuda_device)
+    y, h, ck = _forward(q, return_state=True, checkpoints=True)
+    ref.check_all(dict(y=y, h=h, ckpt=ck), r)
+    ref.check_all(_backward(q, ck), r)
+
+
 @DT
 @pytest.mark.parametrize("shape", [(1, 1, 1, 8), (3, 1, 40, 16), (5, 1, 77, 32), (130, 1, 24, 64)], ids=str)
 def test_step(cuda_device, shape, dtype):
