@@ -100,12 +100,15 @@ __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wai
 template <typename T, int N>
 struct __align__(16) Smem {
   using S = Shape<N>;
-  float4 dxg[kTile][S::kCh];              // (Δ, Δ x, g, x), then (gx, gdt / σ, p, -); columns permuted
+  float4 dxg[kTile][S::kCh];              // (Δ, Δ x, g, x), then (gx, gdt, gz, -); columns permuted
   float bc[2][kTile][4 * N + 16];         // B and C: copy p (at p N) holds state 4 s + i at 4 s + (i ^ p)
   float red[kWarps][kTile][2 * N];        // per warp: gC, gB of a token
   float bias[S::kCh];                     // dt_bias
-  float2 sg[S::kRun][kThreads];           // σ(dt + bias), gy silu'(z): each thread's own
-  float4 snap[kTile / kSub][2][kThreads]; // states before tokens 0, 4, 8, 12, each thread's own
+  float2 sg[kTile][S::kCh];               // (σ(dt + bias), gy silu'(z)), columns permuted
+  // states before tokens 0, 4, 8, 12, each thread's own; then, where it leaves room for three CTAs an
+  // SM, the next tile's checkpoint (else that waits for the first of these to be free)
+  static constexpr bool kEarly = sizeof(T) == 2;
+  float4 snap[kTile / kSub + (kEarly ? 1 : 0)][2][kThreads];
   Stage<T, S::kRun> x, dt, z, gy;
 };
 
@@ -181,9 +184,7 @@ __global__ void __launch_bounds__(kThreads, 3) scan_bwd_kernel(const __grid_cons
   // the loads' view: one token of the tile, a run of channels
   const int lt = tid / TT, lq = tid % TT;
   const int c0 = ct * CH + lq * RUN, nc = max(0, min(RUN, f.C - c0));
-  float gd[RUN], gbias[RUN];
-#pragma unroll
-  for (int i = 0; i < RUN; ++i) gd[i] = gbias[i] = 0.f;
+  float gd = 0.f, gbias = 0.f;  // of channel ch[0], over the tokens whose sums this lane ends up with
 
   for (int i = tid; i < CH; i += kThreads)
     sm.bias[i] = f.dt_bias != nullptr && ct * CH + i < f.C ? f.dt_bias[ct * CH + i] : 0.f;
@@ -191,17 +192,13 @@ __global__ void __launch_bounds__(kThreads, 3) scan_bwd_kernel(const __grid_cons
 
   constexpr int QT = (S::kQuads + kThreads - 1) / kThreads;
   Raw<T, 4> bc[QT];
-  const size_t row0 = (size_t)bb * f.T + lt;
-  const T* x_at = static_cast<const T*>(f.x) + row0 * f.ldx + c0;
-  const T* dt_at = static_cast<const T*>(f.dt) + row0 * f.lddt + c0;
-  const T* gy_at = static_cast<const T*>(p.gy) + row0 * f.C + c0;
-  const T* z_at = f.z != nullptr ? static_cast<const T*>(f.z) + row0 * f.ldz + c0 : nullptr;
   const auto fetch = [&](int ts) {  // a tile's inputs, on their way
     const int n = ts + lt < t1 ? nc : 0;  // n = 0: zeros, nothing read
-    sm.x.fetch(x_at + (ptrdiff_t)ts * f.ldx, n, f.vec);
-    sm.dt.fetch(dt_at + (ptrdiff_t)ts * f.lddt, n, f.vec);
-    sm.gy.fetch(gy_at + (ptrdiff_t)ts * f.C, n, f.vec);
-    if (f.z != nullptr) sm.z.fetch(z_at + (ptrdiff_t)ts * f.ldz, n, f.vec);
+    const size_t row = (size_t)bb * f.T + (ts + lt);
+    sm.x.fetch(static_cast<const T*>(f.x) + row * f.ldx + c0, n, f.vec);
+    sm.dt.fetch(static_cast<const T*>(f.dt) + row * f.lddt + c0, n, f.vec);
+    sm.gy.fetch(static_cast<const T*>(p.gy) + row * f.C + c0, n, f.vec);
+    if (f.z != nullptr) sm.z.fetch(static_cast<const T*>(f.z) + row * f.ldz + c0, n, f.vec);
     cp_async_commit();
 #pragma unroll
     for (int k = 0; k < QT; ++k) {
@@ -214,10 +211,12 @@ __global__ void __launch_bounds__(kThreads, 3) scan_bwd_kernel(const __grid_cons
       bc[k].load(static_cast<const T*>(is_c ? f.c : f.b) + rq * (is_c ? f.ldc : f.ldb) + s0, on ? 4 : 0, f.vec_bc);
     }
   };
-  const auto fetch_state = [&](int ts) {  // the states before token ts, into this thread's first snapshot
+  constexpr bool kEarly = Smem<T, N>::kEarly;
+  constexpr int kCk = kEarly ? kTile / kSub : 0;
+  const auto fetch_state = [&](int ts) {  // the states before token ts
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      float4* dst = &sm.snap[0][j][tid];
+      float4* dst = &sm.snap[kCk][j][tid];
       if (cact[j])
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)),
                      "l"(f.ckpt + (size_t)(ts / kScanCkLen) * plane + hoff[j])
@@ -258,12 +257,11 @@ __global__ void __launch_bounds__(kThreads, 3) scan_bwd_kernel(const __grid_cons
         // behind the end and past the last channel x = gy = 0 were fetched; Δ = 0 keeps the state
         if (!tact || i >= nc) dl.x = 0.f;
         if (!tact || i + 1 >= nc) dl.y = 0.f;
-        const float2 dx = mul2(dl, x), gxx = fma2(g, x, make_float2(gd[i], gd[i + 1]));
-        gd[i] = gxx.x, gd[i + 1] = gxx.y;
+        const float2 dx = mul2(dl, x);
         sm.dxg[lt][S::col(cc)] = make_float4(dl.x, dx.x, g.x, x.x);
         sm.dxg[lt][S::col(cc + 1)] = make_float4(dl.y, dx.y, g.y, x.y);
-        sm.sg[i][tid] = make_float2(sig.x, gpre.x);
-        sm.sg[i + 1][tid] = make_float2(sig.y, gpre.y);
+        sm.sg[lt][S::col(cc)] = make_float2(sig.x, gpre.x);
+        sm.sg[lt][S::col(cc + 1)] = make_float2(sig.y, gpre.y);
       }
     }
 #pragma unroll
@@ -281,11 +279,14 @@ __global__ void __launch_bounds__(kThreads, 3) scan_bwd_kernel(const __grid_cons
     float2 h[2][2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const float4 v = sm.snap[0][j][tid];
+      const float4 v = sm.snap[kCk][j][tid];
       h[j][0] = make_float2(v.x, v.y), h[j][1] = make_float2(v.z, v.w);
       xor_order(h[j], ord);
     }
-    if (ts > t0) fetch(ts - kTile);
+    if (ts > t0) {
+      fetch(ts - kTile);
+      if (kEarly) fetch_state(ts - kTile);
+    }
     __syncthreads();
 
     // the states every 4 tokens
@@ -327,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 3) scan_bwd_kernel(const __grid_cons
           }
         }
       }
-      float sp[kSub], s1[kSub], s2[kSub];
+      float sp[kSub], s1[kSub], s2[kSub], rv[kSub][CP >= 8 ? 1 : CP == 4 ? 2 : 4];
 #pragma unroll
       for (int k = kSub - 1; k >= 0; --k) {
         float2 bv[2], cv[2], vc[2], vb[2];  // vc, vb: this thread's part of gC and gB
@@ -364,7 +365,6 @@ __global__ void __launch_bounds__(kThreads, 3) scan_bwd_kernel(const __grid_cons
         vc[0].y += __shfl_xor_sync(0xffffffffu, vc[1].y, B1);
         vb[0].x += __shfl_xor_sync(0xffffffffu, vb[1].x, B1);
         vb[0].y += __shfl_xor_sync(0xffffffffu, vb[1].y, B1);
-        float* red = sm.red[warp][k0 + k] + sub * kSN;
         if constexpr (CP >= 4) {
           vc[0].x += __shfl_xor_sync(0xffffffffu, vc[0].y, L);
           vb[0].x += __shfl_xor_sync(0xffffffffu, vb[0].y, L);
@@ -373,14 +373,24 @@ __global__ void __launch_bounds__(kThreads, 3) scan_bwd_kernel(const __grid_cons
             float v = up ? vb[0].x : vc[0].x;
             v += __shfl_xor_sync(0xffffffffu, up ? vc[0].x : vb[0].x, 4 * L);
             if constexpr (CP >= 16) v += __shfl_xor_sync(0xffffffffu, v, 8 * L);
-            if (CP == 8 || cl < 8) red[(up ? N : 0) + ord] = v;
+            rv[k][0] = v;
           } else {
-            red[ord] = vc[0].x;
-            red[N + ord] = vb[0].x;
+            rv[k][0] = vc[0].x, rv[k][1] = vb[0].x;
           }
         } else {
-          red[ord] = vc[0].x, red[ord + 1] = vc[0].y;
-          red[N + ord] = vb[0].x, red[N + ord + 1] = vb[0].y;
+          rv[k][0] = vc[0].x, rv[k][1] = vb[0].x;
+          rv[k][2] = vc[0].y, rv[k][3] = vb[0].y;
+        }
+      }
+      // stored behind all four tokens: no load above has to wait for a store to shared memory
+#pragma unroll
+      for (int k = 0; k < kSub; ++k) {
+        float* red = sm.red[warp][k0 + k] + sub * kSN + ord;
+        if constexpr (CP >= 8) {
+          if (CP == 8 || cl < 8) red[(cl & 4) != 0 ? N : 0] = rv[k][0];
+        } else {
+          red[0] = rv[k][0], red[N] = rv[k][1];
+          if constexpr (CP == 2) red[1] = rv[k][2], red[N + 1] = rv[k][3];
         }
       }
       constexpr int HL = L / 2, M = HL < kSub ? HL : kSub;  // lanes that hold one channel; with different tokens
@@ -392,13 +402,17 @@ __global__ void __launch_bounds__(kThreads, 3) scan_bwd_kernel(const __grid_cons
       if (hs < M) {
 #pragma unroll
         for (int k = 0; k < kSub / M; ++k) {
-          float4& d = sm.dxg[k0 + hs * (kSub / M) + k][col[0]];
-          const float4 v = d;
-          d = make_float4(fmaf(v.x, s1[k], dsk * v.z), fmaf(v.w, s1[k], s2[k] * kLn2), fmaf(dsk, v.w, sp[k]), 0.f);
+          const int tk = k0 + hs * (kSub / M) + k;
+          const float4 v = sm.dxg[tk][col[0]];
+          const float2 sg = sm.sg[tk][col[0]];
+          const float gdt = sg.x * fmaf(v.w, s1[k], s2[k] * kLn2);
+          sm.dxg[tk][col[0]] = make_float4(fmaf(v.x, s1[k], dsk * v.z), gdt, sg.y * fmaf(dsk, v.w, sp[k]), 0.f);
+          gd = fmaf(v.z, v.w, gd);
+          if (ts + tk < t1) gbias += gdt;  // a token that is not there has decays of 1 and a sum s2
         }
       }
     }
-    if (ts > t0) fetch_state(ts - kTile);
+    if (!kEarly && ts > t0) fetch_state(ts - kTile);
     __syncthreads();
 
     if (tact && nc > 0) {
@@ -406,11 +420,7 @@ __global__ void __launch_bounds__(kThreads, 3) scan_bwd_kernel(const __grid_cons
 #pragma unroll
       for (int i = 0; i < RUN; ++i) {
         const float4 d = sm.dxg[lt][S::col(lq * RUN + i)];
-        const float2 sg = sm.sg[i][tid];
-        ox[i] = d.x;
-        odt[i] = sg.x * d.y;
-        gbias[i] += odt[i];  // 0 for a token or channel that is not there
-        oz[i] = sg.y * d.z;
+        ox[i] = d.x, odt[i] = d.y, oz[i] = d.z;
       }
       const size_t off = ((size_t)bb * f.T + ts + lt) * f.C + c0;
       store_part<T, RUN>(static_cast<T*>(p.gx) + off, nc, f.vec, ox);
@@ -427,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, 3) scan_bwd_kernel(const __grid_cons
       if (ts + tk < t1) part[i] = s;
     }
     // no barrier: the next tile's stores before its own barrier go only where this thread alone
-    // still reads (its run's columns of dxg, sg, its stages) or nobody does (bc)
+    // still reads (its run's columns of dxg, its stages) or nobody does (bc)
   }
 
   const size_t prow = (size_t)bb * f.nseg + seg;
@@ -439,25 +449,15 @@ __global__ void __launch_bounds__(kThreads, 3) scan_bwd_kernel(const __grid_cons
     store_pairs<2>(p.part_a + (prow * f.C + ct * CH + ch[j]) * N + sub * kSN, ga[j]);
     if (seg == 0 && p.gh_in != nullptr) store_pairs<2>(p.gh_in + hoff[j], gh[j]);
   }
-  // gd and gdt_bias: the 16 tokens of a run of channels meet in shared memory
-  __syncthreads();
-  float* s_gd = reinterpret_cast<float*>(sm.dxg);  // [16][CH] each
-  float* s_gb = s_gd + kTile * CH;
+  // gd and gdt_bias: over the lanes that hold a channel's tokens
 #pragma unroll
-  for (int i = 0; i < RUN; ++i) {
-    s_gd[lt * CH + lq * RUN + i] = gd[i];
-    s_gb[lt * CH + lq * RUN + i] = gbias[i];
+  for (int o = L / 4; o > 0; o >>= 1) {
+    gd += __shfl_xor_sync(0xffffffffu, gd, o);
+    gbias += __shfl_xor_sync(0xffffffffu, gbias, o);
   }
-  __syncthreads();
-  if (tid < CH && ct * CH + tid < f.C) {
-    float a = 0.f, b = 0.f;
-#pragma unroll
-    for (int k = 0; k < kTile; ++k) {
-      a += s_gd[k * CH + tid];
-      b += s_gb[k * CH + tid];
-    }
-    p.part_v[(prow * 2 + 0) * f.C + ct * CH + tid] = a;
-    p.part_v[(prow * 2 + 1) * f.C + ct * CH + tid] = b;
+  if (sub % (L / 2) == 0 && cact[0]) {
+    p.part_v[(prow * 2 + 0) * f.C + ct * CH + ch[0]] = gd;
+    p.part_v[(prow * 2 + 1) * f.C + ct * CH + ch[0]] = gbias;
   }
 }
 
