@@ -213,7 +213,7 @@ cudaError_t launch_wkv5_bwd_reduce(int B, int H, const double* part_fwd, const d
 struct ConvParams {
   int B, T, C, W;       // W in 2..4
   int silu;             // 1: y = silu(pre)
-  int nseg;             // stretches of tokens per batch row (set by the launch)
+  int stretch, nseg;    // tokens per stretch, stretches per batch row (set by the launch)
   long long ldx;
   const float* weight;  // [C,W]
   const float* bias;    // [C] or null
