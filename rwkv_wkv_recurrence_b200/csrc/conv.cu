@@ -14,6 +14,10 @@
 // 8 at a time and left as loaded until they are due.  V is small (8 bytes a load forward, 4 to 8
 // backward, whose two windows and W+1 sums are kept besides) so that enough threads fit on an SM to
 // keep its loads in flight.  Neighbouring stretches re-read W-1 tokens, which come from L2.
+// At 4x4096x2560 bf16, W = 4: forward 32 us (5.2 TB/s, 82 % of a copy's rate), backward 64 + 4 us of
+// reduction (3.9 TB/s; about half of its cycles issue, and two CTAs of 128 registers a thread fill an
+// SM).  Fetching 4 or 12 tokens together in the backward, or 4 channels a thread, measured 3 to 25 %
+// slower.
 #include "launch.h"
 #include "mixer_common.cuh"
 

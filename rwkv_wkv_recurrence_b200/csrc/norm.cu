@@ -11,12 +11,14 @@
 // would save no pass over the data.
 //
 // One pass over the data, so bandwidth bounds it.  A team of 8 to 512 threads holds one group of a
-// row in registers (1 or 2 vectors a thread): the variance is the mean of (x - mean)², not a
+// row in registers (1 to 3 vectors a thread): the variance is the mean of (x - mean)², not a
 // difference of large sums.  A team keeps its group and strides over the rows, so w and b, and the
 // backward's column sums, stay in registers; teams of neighbouring groups are neighbours, so a
 // CTA's accesses are contiguous.  Column sums go to the workspace per team and are added in order
 // by a second kernel: no atomics, the same inputs give the same bits.  Groups wider than 1024
-// vectors take a kernel that reads the row again for each sum (from L1 / L2).
+// vectors take a kernel that reads the row again for each sum (from L1 / L2).  Rows are fetched a turn
+// ahead.  Measured: gated heads 16384x40x64 bf16 46 us forward (5.5 TB/s, 85 % of a copy's rate),
+// 83 + 8 us backward (5.1 TB/s); fp32 8192x768 9.7 us and 16 + 6 us.
 #include <algorithm>
 
 #include "launch.h"

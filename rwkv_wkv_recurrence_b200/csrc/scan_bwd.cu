@@ -11,10 +11,15 @@
 // checkpoint and kept every 4 tokens; then, from the last 4 tokens to the first, the 4 states and
 // decays are formed again in registers and walked backwards with G.
 //
-// What bounds it: the shared-memory pipe and the issue slots.  Every lane needs B_t[n] and C_t[n] of
-// its states, and a load costs that pipe 4 bytes a lane and turn even where all lanes read the same
-// words, so a thread owns 4 states of TWO channels and each loaded word serves both (one channel per
-// thread needed 9.3 turns per state and token, two 6).  N/4 neighbouring lanes own a channel pair.
+// What bounds it: latency and the shared-memory pipe together.  At 4x4096x2560, N = 16, bf16 the main
+// kernel takes 0.83 ms; 12 warps an SM (168 registers, 70 KB a CTA) issue in 52 % of the cycles, the
+// shared-memory pipe is busy 64 %, the special-function unit 37 %.  16 warps an SM (128 registers,
+// the decays formed twice) measured 0.85 ms, 8 with 255 registers 0.93, unpacked arithmetic 0.85
+// (a third more instructions, 67 % of the cycles).  Every lane needs B_t[n] and C_t[n] of its states,
+// and a load costs the shared-memory pipe 4 bytes a lane and turn even where all lanes read the same
+// words, so a thread owns 4 states of TWO channels and each loaded word serves both; N/4 neighbouring
+// lanes own a channel pair.  (One channel per thread, with selects in its exchanges and the loads
+// waited for where they were issued, took 3.9 ms in all.)
 //   - Sums over a pair's states (p, s1, s2): half of a pair's lanes hold its two channels in the
 //     other order, so the first exchange gives away one channel and keeps the other without selects.
 //   - Sums over channels (gB, gC: all channels share B and C): the lanes hold their 4 states in an
@@ -22,7 +27,8 @@
 //     orders), so that the exchanges need no selects either; warps meet in shared memory, CTAs in the
 //     workspace, added by a last kernel.  No atomics: the same inputs give the same bits.
 //   - x, dt, z, gy and the checkpoint arrive by cp.async, a tile ahead, each thread reading back what
-//     it fetched.
+//     it fetched; stores to shared memory wait until four tokens are done, so that no load of the next
+//     token queues behind one.
 //
 // Time is cut into segments so that the CTAs fill the SMs evenly; the carry G that enters a segment
 // from behind is folded from the later segments' own (each from zero, by a first launch of
@@ -474,6 +480,21 @@ __global__ void __launch_bounds__(256) scan_bwd_bc_kernel(int ctiles, size_t n, 
   (j < N ? gc : gb)[row * N + j % N] = IO<T>::from_f(s);
 }
 
+// n floats `stride` apart, added in order, 8 loads at a time.
+__device__ __forceinline__ double sum_parts(const float* __restrict__ p, int n, size_t stride) {
+  double s = 0.0;
+  int k = 0;
+  for (; k + 8 <= n; k += 8) {
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = p[(size_t)(k + i) * stride];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s += (double)v[i];
+  }
+  for (; k < n; ++k) s += (double)p[(size_t)k * stride];
+  return s;
+}
+
 // ga_log [C,N], then gd [C] and gdt_bias [C]: the parts of the batch rows and segments in order.
 __global__ void __launch_bounds__(256) scan_bwd_param_kernel(int nparts, int C, int N, const float* __restrict__ a_log,
                                                              const float* __restrict__ part_a,
@@ -481,16 +502,11 @@ __global__ void __launch_bounds__(256) scan_bwd_param_kernel(int nparts, int C, 
                                                              float* gdt_bias) {
   const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x, na = (size_t)C * N;
   if (i < na) {
-    double s = 0.0;
-    for (int k = 0; k < nparts; ++k) s += (double)part_a[(size_t)k * na + i];
-    ga_log[i] = (float)(s * -(double)expf(a_log[i]));
+    ga_log[i] = (float)(sum_parts(part_a + i, nparts, na) * -(double)expf(a_log[i]));
   } else if (i < na + 2 * (size_t)C) {
     const size_t j = i - na;
     float* dst = j < (size_t)C ? gd : gdt_bias;
-    if (dst == nullptr) return;
-    double s = 0.0;
-    for (int k = 0; k < nparts; ++k) s += (double)part_v[(size_t)k * 2 * C + j];
-    dst[j % C] = (float)s;
+    if (dst != nullptr) dst[j % C] = (float)sum_parts(part_v + j, nparts, 2 * (size_t)C);
   }
 }
 

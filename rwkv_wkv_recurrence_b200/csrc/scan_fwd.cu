@@ -5,9 +5,12 @@
 //   p_t = Σ_n C_t[n] h_t[n] + d x_t,   y_t = p_t, or p_t z_t σ(z_t) with a gate z.
 // B_t and C_t are shared by all channels of a token.
 //
-// What bounds it: one exponential per state and token.  With N = 16 an element (b, t, c) moves
-// 8 bytes in bf16 but needs 16 ex2, and the special-function unit does 16 a clock and SM, so the
-// exponentials take about three times as long as the bytes.
+// What bounds it: one exponential per state and token, and the shared-memory pipe.  With N = 16 an
+// element (b, t, c) moves 8 bytes in bf16 but needs 16 ex2, and the special-function unit does 16 a
+// clock and SM: 0.15 ms at 4x4096x2560, where the bytes take 0.05.  The same work takes that pipe
+// about 14 turns per warp and token of 4 states a lane (4 bytes a lane and turn), half again as long:
+// with enough channels it is 93 % busy (8x4096x5120: 1.12 ms); at 4x4096x2560 (0.38 ms) only ten warps
+// an SM share it and latency counts as much.
 //
 // Mapping.  A thread owns 4 states of one channel, the lanes of a warp are channels; a CTA owns 16
 // or 32 channels of one batch row over one time segment, 32 tokens at a time:
@@ -17,13 +20,15 @@
 //      fp32 rows;
 //   2. each thread walks the 32 tokens, reading 4 of them ahead; Σ_n over its 4 states goes to
 //      shared memory per group of states (folding a channel's states over lanes instead costs
-//      three shuffles and nine selects and adds per 4 tokens, and measured 0.473 ms);
+//      three shuffles and nine selects and adds per 4 tokens, and measured 0.473 ms; two channels
+//      a thread, to use each B and C twice, 0.49: too few warps; half of the CTA for loads and
+//      outputs, half for the scan, 0.44);
 //   3. the tile's outputs add the groups' sums, d x and the gate and leave in the same runs.
 //
 // Few channels, long axis: time is cut into segments.  A first launch runs every segment but the
 // last from a zero state and keeps the state it reaches and ΣΔ; the state entering segment s is
 // then folded from these in order (the decay over a segment is exp(A ΣΔ)) by the CTA that needs
-// it, in the second launch, which writes the outputs.  Sums run in a fixed order: the same inputs
+// it, in the second launch, which writes the outputs (1x8192x2048: 0.37 ms whole, 0.21 in 9 segments).  Sums run in a fixed order: the same inputs
 // give the same bits.
 #include <algorithm>
 

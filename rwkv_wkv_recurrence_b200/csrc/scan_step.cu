@@ -1,8 +1,9 @@
 // Selective scan, one token for each of B independent streams (sm_100a): scan_fwd.cu's recurrence
 // with T = 1.  A pass over the fp32 state [B,C,N] (read once, written once), which bounds it; a
-// thread owns 4 states of one channel (16-byte accesses), N/4 neighbouring lanes a channel, for
-// kStreams streams, whose loads are in flight together and share the channel's rates.  A thread
-// reads its states before it writes them, so h_out may be h_in.
+// thread owns 4 states of one channel (16-byte accesses), N/4 neighbouring lanes a channel.  With many
+// streams all CTAs fit at once and take the streams in turn, the next two's inputs in flight while two
+// are worked on: 512x2560, N = 16, bf16 38.5 us (4.6 TB/s, 72 % of a copy's rate; one stream a thread
+// and a CTA 59 us).  A thread reads its states before it writes them, so h_out may be h_in.
 #include <algorithm>
 
 #include "launch.h"
