@@ -508,25 +508,28 @@ def _io_code(name, t):
     raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
 
 
-def _dense(name, t, shape, dtype, device):
-    """t (or None) is a contiguous tensor of this shape, type and device."""
-    if t is None:
-        return
+def _refuse(name, t, shape, dtype, index):
     if t.dtype != dtype or t.shape != shape:
         raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected the device of the other tensors")
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _rows(name, t, shape, dtype, device):
+def _dense(name, t, shape, dtype, index):
+    """t (or None) is a contiguous tensor of this shape and type on device `index`; its address."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+        _refuse(name, t, shape, dtype, index)
+    return t.data_ptr()
+
+
+def _rows(name, t, shape, dtype, index):
     """Elements between the rows of t, whose last dimension is dense and whose rows lie at equal
     distances (a whole tensor, or a part of a wider one's last dimension)."""
-    if t.dtype != dtype or t.shape != shape:
-        raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index:
+        _refuse(name, t, shape, dtype, index)
     width = shape[-1]
     if t.is_contiguous():
         return width
@@ -554,64 +557,74 @@ def _dims(name, t, n):
     return t.shape
 
 
-class _Launch:
-    """The stream a call launches on, and the call's allocations, which belong to that stream.  Where
-    it is not the current one, the tensors that the two share are recorded on both, so that memory
-    freed after the call is not handed out again too early."""
+class _Elsewhere:
+    """A call that launches on another stream than the current one: its allocations belong to that
+    stream, and the tensors the two share are recorded on both, so that memory freed after the call
+    is not handed out again too early."""
 
-    __slots__ = ("x", "raw", "stream", "outputs")
+    def __init__(self, stream):
+        self.stream, self.outputs = stream, []
 
-    def __init__(self, x, stream):
+    def empty(self, x, shape, dtype, output):
         import torch
 
-        if not x.is_cuda:
-            raise ValueError("tensors must be CUDA tensors (use .cuda())")
-        index, current = x.get_device(), torch._C._cuda_getDevice()
-        if index != current:
-            raise ValueError(f"tensors are on {x.device}, the current device is cuda:{current}")
-        self.x = x
-        self.raw = torch._C._cuda_getCurrentRawStream(index)
-        self.stream = None  # set where the launch is not on the current stream
-        if stream is not None:
-            if stream.device.index != index:
-                raise ValueError(f"stream is on {stream.device}, the tensors on {x.device}")
-            if stream.cuda_stream != self.raw:
-                self.stream, self.raw, self.outputs = stream, stream.cuda_stream, []
-
-    def like(self):
-        """An output shaped and typed like x, contiguous."""
-        import torch
-
-        if self.stream is None:
-            return torch.empty_like(self.x, memory_format=torch.contiguous_format)
-        return self.empty(self.x.shape, self.x.dtype)
-
-    def empty(self, shape, dtype, output=True):
-        import torch
-
-        if self.stream is None:
-            return self.x.new_empty(shape, dtype=dtype)
         with torch.cuda.stream(self.stream):
-            t = self.x.new_empty(shape, dtype=dtype)
+            t = x.new_empty(shape, dtype=dtype)
         if output:
             self.outputs.append(t)
         return t
 
-    def workspace(self, nbytes):
-        import torch
-
-        return self.empty((nbytes,), torch.uint8, output=False) if nbytes else None
-
     def done(self, *given):
         import torch
 
-        if self.stream is not None:
-            current = torch.cuda.current_stream()
-            for t in self.outputs:
-                t.record_stream(current)
-            for t in given:
-                if t is not None:
-                    t.record_stream(self.stream)
+        current = torch.cuda.current_stream()
+        for t in self.outputs:
+            t.record_stream(current)
+        for t in given:
+            if t is not None:
+                t.record_stream(self.stream)
+
+
+def _launch(x, stream):
+    """The device index of x, the stream handle a call launches on, and an ``_Elsewhere`` where that is
+    not the current stream (else None)."""
+    import torch
+
+    index = x.get_device()
+    if index < 0:
+        raise ValueError("tensors must be CUDA tensors (use .cuda())")
+    current = torch._C._cuda_getDevice()
+    if index != current:
+        raise ValueError(f"tensors are on {x.device}, the current device is cuda:{current}")
+    raw = torch._C._cuda_getCurrentRawStream(index)
+    if stream is None:
+        return index, raw, None
+    if stream.device.index != index:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {x.device}")
+    if stream.cuda_stream == raw:
+        return index, raw, None
+    return index, stream.cuda_stream, _Elsewhere(stream)
+
+
+def _like(x, other):
+    """An output shaped and typed like x, contiguous."""
+    import torch
+
+    if other is None:
+        return torch.empty_like(x, memory_format=torch.contiguous_format)
+    return other.empty(x, x.shape, x.dtype, True)
+
+
+def _empty(x, shape, dtype, other):
+    return x.new_empty(shape, dtype=dtype) if other is None else other.empty(x, shape, dtype, True)
+
+
+def _workspace(x, nbytes, other):
+    import torch
+
+    if not nbytes:
+        return None
+    return x.new_empty(nbytes, dtype=torch.uint8) if other is None else other.empty(x, (nbytes,), torch.uint8, False)
 
 
 def rwkv_causal_conv_forward(x, weight, bias=None, state_in=None, *, silu=False, return_state=False, stream=None,
@@ -624,22 +637,23 @@ def rwkv_causal_conv_forward(x, weight, bias=None, state_in=None, *, silu=False,
     last W-1 tokens [B,W-1,C] if ``return_state``."""
     import torch
 
-    L, dev, dt = _Launch(x, stream), x.device, x.dtype
+    (dev, raw, other), dt = _launch(x, stream), x.dtype
     code = _io_code("x", x)
     B, T, C = _dims("x", x, 3)
     W = _dims("weight", weight, 2)[1]
-    _dense("weight", weight, (C, W), torch.float32, dev)
-    _dense("bias", bias, (C,), torch.float32, dev)
-    _dense("state_in", state_in, (B, W - 1, C), dt, dev)
+    p_weight = _dense("weight", weight, (C, W), torch.float32, dev)
+    p_bias = _dense("bias", bias, (C,), torch.float32, dev)
+    p_state_in = _dense("state_in", state_in, (B, W - 1, C), dt, dev)
     _dense("out", out, (B, T, C), dt, dev)
     ldx = _rows("x", x, (B, T, C), dt, dev)
-    y = L.like() if out is None else out
-    st = L.empty((B, W - 1, C), dt) if return_state and W > 0 else None
+    y = _like(x, other) if out is None else out
+    st = _empty(x, (B, W - 1, C), dt, other) if return_state and W > 0 else None
     _check("rwkv_causal_conv_forward",
-           _fn("rwkv_causal_conv_forward")(B, T, C, W, code, _addr(weight), _addr(bias),
-                                           ACT_SILU if silu else ACT_NONE, _addr(x), ldx, _addr(y), _addr(state_in),
-                                           _addr(st), L.raw))
-    L.done(x, weight, bias, state_in, out)
+           _fn("rwkv_causal_conv_forward")(B, T, C, W, code, p_weight, p_bias,
+                                           ACT_SILU if silu else ACT_NONE, _addr(x), ldx, _addr(y), p_state_in,
+                                           _addr(st), raw))
+    if other is not None:
+        other.done(x, weight, bias, state_in, out)
     return (y, st) if return_state else y
 
 
@@ -650,28 +664,29 @@ def rwkv_causal_conv_backward(x, weight, gy, bias=None, state_in=None, gstate_ou
     gbias is None where bias is."""
     import torch
 
-    L, dev, dt = _Launch(x, stream), x.device, x.dtype
+    (dev, raw, other), dt = _launch(x, stream), x.dtype
     code = _io_code("x", x)
     B, T, C = _dims("x", x, 3)
     W = _dims("weight", weight, 2)[1]
-    _dense("weight", weight, (C, W), torch.float32, dev)
-    _dense("bias", bias, (C,), torch.float32, dev)
-    _dense("gy", gy, (B, T, C), dt, dev)
-    _dense("state_in", state_in, (B, W - 1, C), dt, dev)
-    _dense("gstate_out", gstate_out, (B, W - 1, C), dt, dev)
+    p_weight = _dense("weight", weight, (C, W), torch.float32, dev)
+    p_bias = _dense("bias", bias, (C,), torch.float32, dev)
+    p_gy = _dense("gy", gy, (B, T, C), dt, dev)
+    p_state_in = _dense("state_in", state_in, (B, W - 1, C), dt, dev)
+    p_gstate_out = _dense("gstate_out", gstate_out, (B, W - 1, C), dt, dev)
     ldx = _rows("x", x, (B, T, C), dt, dev)
-    gx = L.like()
-    gw = L.empty((C, W), torch.float32)
-    gb = L.empty((C,), torch.float32) if bias is not None else None
-    gs = L.empty((B, W - 1, C), dt) if want_gstate_in and W > 0 else None
+    gx = _like(x, other)
+    gw = _empty(x, (C, W), torch.float32, other)
+    gb = _empty(x, (C,), torch.float32, other) if bias is not None else None
+    gs = _empty(x, (B, W - 1, C), dt, other) if want_gstate_in and W > 0 else None
     wsb = _fn("rwkv_causal_conv_backward_workspace_bytes")(B, T, C, W)
-    ws = L.workspace(wsb)
+    ws = _workspace(x, wsb, other)
     _check("rwkv_causal_conv_backward",
-           _fn("rwkv_causal_conv_backward")(B, T, C, W, code, _addr(weight), _addr(bias),
-                                            ACT_SILU if silu else ACT_NONE, _addr(x), ldx, _addr(state_in), _addr(gy),
-                                            _addr(gstate_out), _addr(gx), _addr(gw), _addr(gb), _addr(gs), _addr(ws),
-                                            wsb, L.raw))
-    L.done(x, weight, gy, bias, state_in, gstate_out)
+           _fn("rwkv_causal_conv_backward")(B, T, C, W, code, p_weight, p_bias,
+                                            ACT_SILU if silu else ACT_NONE, _addr(x), ldx, p_state_in, p_gy,
+                                            p_gstate_out, _addr(gx), _addr(gw), _addr(gb), _addr(gs), _addr(ws),
+                                            wsb, raw))
+    if other is not None:
+        other.done(x, weight, gy, bias, state_in, gstate_out)
     return (gx, gw, gb, gs) if want_gstate_in else (gx, gw, gb)
 
 
@@ -680,36 +695,37 @@ def rwkv_causal_conv_step(x, weight, state, bias=None, *, silu=False, state_out=
     ``state_out`` is given.  Returns y [B,C]."""
     import torch
 
-    L, dev, dt = _Launch(x, stream), x.device, x.dtype
+    (dev, raw, other), dt = _launch(x, stream), x.dtype
     code = _io_code("x", x)
     B, C = _dims("x", x, 2)
     W = _dims("weight", weight, 2)[1]
-    _dense("weight", weight, (C, W), torch.float32, dev)
-    _dense("bias", bias, (C,), torch.float32, dev)
-    _dense("state", state, (B, W - 1, C), dt, dev)
+    p_weight = _dense("weight", weight, (C, W), torch.float32, dev)
+    p_bias = _dense("bias", bias, (C,), torch.float32, dev)
+    p_state = _dense("state", state, (B, W - 1, C), dt, dev)
     _dense("state_out", state_out, (B, W - 1, C), dt, dev)
     _dense("out", out, (B, C), dt, dev)
     ldx = _rows("x", x, (B, C), dt, dev)
-    y = L.like() if out is None else out
+    y = _like(x, other) if out is None else out
     so = state if state_out is None else state_out
     _check("rwkv_causal_conv_step",
-           _fn("rwkv_causal_conv_step")(B, C, W, code, _addr(weight), _addr(bias), ACT_SILU if silu else ACT_NONE,
-                                        _addr(x), ldx, _addr(y), _addr(state), _addr(so), L.raw))
-    L.done(x, weight, state, bias, state_out, out)
+           _fn("rwkv_causal_conv_step")(B, C, W, code, p_weight, p_bias, ACT_SILU if silu else ACT_NONE,
+                                        _addr(x), ldx, _addr(y), p_state, _addr(so), raw))
+    if other is not None:
+        other.done(x, weight, state, bias, state_out, out)
     return y
 
 
-def _scan_args(x, dt, b, c, a_log, d, dt_bias, z):
+def _scan_args(x, dt, b, c, a_log, d, dt_bias, z, dev):
     """Checks what the scan's calls share; returns N and the C calls' arguments from a_log to ldz."""
     import torch
 
-    lead, C, dev, ty = x.shape[:-1], x.shape[-1], x.device, x.dtype
+    lead, C, ty = x.shape[:-1], x.shape[-1], x.dtype
     N = _dims("a_log", a_log, 2)[1]
-    _dense("a_log", a_log, (C, N), torch.float32, dev)
-    _dense("d", d, (C,), torch.float32, dev)
-    _dense("dt_bias", dt_bias, (C,), torch.float32, dev)
+    p_a_log = _dense("a_log", a_log, (C, N), torch.float32, dev)
+    p_d = _dense("d", d, (C,), torch.float32, dev)
+    p_dt_bias = _dense("dt_bias", dt_bias, (C,), torch.float32, dev)
     wide, state = lead + (C,), lead + (N,)
-    return N, (_addr(a_log), _addr(d), _addr(dt_bias),
+    return N, (p_a_log, p_d, p_dt_bias,
                _addr(x), _rows("x", x, wide, ty, dev), _addr(dt), _rows("dt", dt, wide, ty, dev),
                _addr(b), _rows("b", b, state, ty, dev), _addr(c), _rows("c", c, state, ty, dev),
                _addr(z), _rows("z", z, wide, ty, dev) if z is not None else C)
@@ -726,21 +742,22 @@ def rwkv_selective_scan_forward(x, dt, b, c, a_log, d=None, dt_bias=None, z=None
     ``rwkv_selective_scan_backward`` if ``checkpoints``."""
     import torch
 
-    L, dev, ty = _Launch(x, stream), x.device, x.dtype
+    (dev, raw, other), ty = _launch(x, stream), x.dtype
     code = _io_code("x", x)
     B, T, C = _dims("x", x, 3)
-    N, args = _scan_args(x, dt, b, c, a_log, d, dt_bias, z)
-    _dense("h_in", h_in, (B, C, N), torch.float32, dev)
+    N, args = _scan_args(x, dt, b, c, a_log, d, dt_bias, z, dev)
+    p_h_in = _dense("h_in", h_in, (B, C, N), torch.float32, dev)
     _dense("out", out, (B, T, C), ty, dev)
-    y = L.like() if out is None else out
-    ho = L.empty((B, C, N), torch.float32) if return_state else None
-    ck = L.empty(((T + CHUNK_LEN - 1) // CHUNK_LEN, B, C, N), torch.float32) if checkpoints else None
+    y = _like(x, other) if out is None else out
+    ho = _empty(x, (B, C, N), torch.float32, other) if return_state else None
+    ck = _empty(x, ((T + CHUNK_LEN - 1) // CHUNK_LEN, B, C, N), torch.float32, other) if checkpoints else None
     wsb = _fn("rwkv_selective_scan_forward_workspace_bytes")(B, T, C, N, algo)
-    ws = L.workspace(wsb)
+    ws = _workspace(x, wsb, other)
     _check("rwkv_selective_scan_forward",
-           _fn("rwkv_selective_scan_forward")(B, T, C, N, code, *args, _addr(y), _addr(h_in), _addr(ho), _addr(ck),
-                                              CHUNK_LEN, algo, _addr(ws), wsb, L.raw))
-    L.done(x, dt, b, c, a_log, d, dt_bias, z, h_in, out)
+           _fn("rwkv_selective_scan_forward")(B, T, C, N, code, *args, _addr(y), p_h_in, _addr(ho), _addr(ck),
+                                              CHUNK_LEN, algo, _addr(ws), wsb, raw))
+    if other is not None:
+        other.done(x, dt, b, c, a_log, d, dt_bias, z, h_in, out)
     res = (y,)
     if return_state:
         res += (ho,)
@@ -757,30 +774,31 @@ def rwkv_selective_scan_backward(x, dt, b, c, a_log, gy, d=None, dt_bias=None, z
     checkpoints, or None to form them again (from ``h_in``)."""
     import torch
 
-    L, dev, ty = _Launch(x, stream), x.device, x.dtype
+    (dev, raw, other), ty = _launch(x, stream), x.dtype
     code = _io_code("x", x)
     B, T, C = _dims("x", x, 3)
-    N, args = _scan_args(x, dt, b, c, a_log, d, dt_bias, z)
+    N, args = _scan_args(x, dt, b, c, a_log, d, dt_bias, z, dev)
     f32 = torch.float32
-    _dense("gy", gy, (B, T, C), ty, dev)
-    _dense("ckpt", ckpt, ((T + CHUNK_LEN - 1) // CHUNK_LEN, B, C, N), f32, dev)
-    _dense("h_in", h_in, (B, C, N), f32, dev)
-    _dense("gh_out", gh_out, (B, C, N), f32, dev)
-    gx, gdt = L.like(), L.like()
-    gb, gc = L.empty((B, T, N), ty), L.empty((B, T, N), ty)
-    gz = L.like() if z is not None else None
-    ga = L.empty((C, N), f32)
-    gd = L.empty((C,), f32) if d is not None else None
-    gbias = L.empty((C,), f32) if dt_bias is not None else None
-    ghi = L.empty((B, C, N), f32) if want_gh_in else None
+    p_gy = _dense("gy", gy, (B, T, C), ty, dev)
+    p_ckpt = _dense("ckpt", ckpt, ((T + CHUNK_LEN - 1) // CHUNK_LEN, B, C, N), f32, dev)
+    p_h_in = _dense("h_in", h_in, (B, C, N), f32, dev)
+    p_gh_out = _dense("gh_out", gh_out, (B, C, N), f32, dev)
+    gx, gdt = _like(x, other), _like(x, other)
+    gb, gc = _empty(x, (B, T, N), ty, other), _empty(x, (B, T, N), ty, other)
+    gz = _like(x, other) if z is not None else None
+    ga = _empty(x, (C, N), f32, other)
+    gd = _empty(x, (C,), f32, other) if d is not None else None
+    gbias = _empty(x, (C,), f32, other) if dt_bias is not None else None
+    ghi = _empty(x, (B, C, N), f32, other) if want_gh_in else None
     wsb = _fn("rwkv_selective_scan_backward_workspace_bytes")(B, T, C, N, CHUNK_LEN, 1 if ckpt is not None else 0)
-    ws = L.workspace(wsb)
+    ws = _workspace(x, wsb, other)
     _check("rwkv_selective_scan_backward",
-           _fn("rwkv_selective_scan_backward")(B, T, C, N, code, *args, _addr(gy), _addr(h_in), _addr(gh_out),
-                                               _addr(ckpt), CHUNK_LEN, _addr(gx), _addr(gdt), _addr(gb), _addr(gc),
+           _fn("rwkv_selective_scan_backward")(B, T, C, N, code, *args, p_gy, p_h_in, p_gh_out,
+                                               p_ckpt, CHUNK_LEN, _addr(gx), _addr(gdt), _addr(gb), _addr(gc),
                                                _addr(gz), _addr(ga), _addr(gd), _addr(gbias), _addr(ghi), _addr(ws),
-                                               wsb, L.raw))
-    L.done(x, dt, b, c, a_log, gy, d, dt_bias, z, ckpt, h_in, gh_out)
+                                               wsb, raw))
+    if other is not None:
+        other.done(x, dt, b, c, a_log, gy, d, dt_bias, z, ckpt, h_in, gh_out)
     res = (gx, gdt, gb, gc, ga, gd, gbias, gz)
     return res + (ghi,) if want_gh_in else res
 
@@ -791,26 +809,27 @@ def rwkv_selective_scan_step(x, dt, b, c, a_log, state, d=None, dt_bias=None, z=
     place unless ``state_out`` is given.  Returns y [B,C]."""
     import torch
 
-    L, dev, ty = _Launch(x, stream), x.device, x.dtype
+    (dev, raw, other), ty = _launch(x, stream), x.dtype
     code = _io_code("x", x)
     B, C = _dims("x", x, 2)
-    N, args = _scan_args(x, dt, b, c, a_log, d, dt_bias, z)
-    _dense("state", state, (B, C, N), torch.float32, dev)
+    N, args = _scan_args(x, dt, b, c, a_log, d, dt_bias, z, dev)
+    p_state = _dense("state", state, (B, C, N), torch.float32, dev)
     _dense("state_out", state_out, (B, C, N), torch.float32, dev)
     _dense("out", out, (B, C), ty, dev)
-    y = L.like() if out is None else out
+    y = _like(x, other) if out is None else out
     so = state if state_out is None else state_out
     _check("rwkv_selective_scan_step",
-           _fn("rwkv_selective_scan_step")(B, C, N, code, *args, _addr(y), _addr(state), _addr(so), L.raw))
-    L.done(x, dt, b, c, a_log, state, d, dt_bias, z, state_out, out)
+           _fn("rwkv_selective_scan_step")(B, C, N, code, *args, _addr(y), p_state, _addr(so), raw))
+    if other is not None:
+        other.done(x, dt, b, c, a_log, state, d, dt_bias, z, state_out, out)
     return y
 
 
-def _norm_args(x, weight, bias, gate, groups):
+def _norm_args(x, weight, bias, gate, groups, dev):
     """Checks what the norm's calls share; returns (M, N) for `groups` groups in x's last dimension."""
     import torch
 
-    shape, dev = x.shape, x.device
+    shape = x.shape
     if len(shape) == 0:
         raise ValueError("x must have at least one dimension")
     C = shape[-1]
@@ -828,15 +847,16 @@ def rwkv_layer_norm_forward(x, weight, bias=None, gate=None, *, groups=1, eps=1e
     (x - mean) / sqrt(var + eps) * weight + bias, times silu(gate) if a gate (like x) is given.
     x fp32 or bf16; weight, bias [C] fp32.  groups = H on an Eagle or Finch output [B,T,H*64] is
     the head-wise norm."""
-    L = _Launch(x, stream)
+    dev, raw, other = _launch(x, stream)
     code = _io_code("x", x)
-    M, N = _norm_args(x, weight, bias, gate, groups)
-    _dense("out", out, x.shape, x.dtype, x.device)
-    y = L.like() if out is None else out
+    M, N = _norm_args(x, weight, bias, gate, groups, dev)
+    _dense("out", out, x.shape, x.dtype, dev)
+    y = _like(x, other) if out is None else out
     _check("rwkv_layer_norm_forward",
            _fn("rwkv_layer_norm_forward")(M, groups, N, code, _addr(weight), _addr(bias), eps, _addr(x), _addr(gate),
-                                          _addr(y), L.raw))
-    L.done(x, weight, bias, gate, out)
+                                          _addr(y), raw))
+    if other is not None:
+        other.done(x, weight, bias, gate, out)
     return y
 
 
@@ -845,22 +865,23 @@ def rwkv_layer_norm_backward(x, weight, gy, bias=None, gate=None, *, groups=1, e
     gbias and ggate are None where bias and gate are."""
     import torch
 
-    L = _Launch(x, stream)
+    dev, raw, other = _launch(x, stream)
     code = _io_code("x", x)
-    M, N = _norm_args(x, weight, bias, gate, groups)
-    _dense("gy", gy, x.shape, x.dtype, x.device)
+    M, N = _norm_args(x, weight, bias, gate, groups, dev)
+    p_gy = _dense("gy", gy, x.shape, x.dtype, dev)
     C = x.shape[-1]
-    gx = L.like()
-    gw = L.empty((C,), torch.float32)
-    gb = L.empty((C,), torch.float32) if bias is not None else None
-    gg = L.like() if gate is not None else None
+    gx = _like(x, other)
+    gw = _empty(x, (C,), torch.float32, other)
+    gb = _empty(x, (C,), torch.float32, other) if bias is not None else None
+    gg = _like(x, other) if gate is not None else None
     wsb = _fn("rwkv_layer_norm_backward_workspace_bytes")(M, groups, N, code)
-    ws = L.workspace(wsb)
+    ws = _workspace(x, wsb, other)
     _check("rwkv_layer_norm_backward",
            _fn("rwkv_layer_norm_backward")(M, groups, N, code, _addr(weight), _addr(bias), eps, _addr(x), _addr(gate),
-                                           _addr(gy), _addr(gx), _addr(gg), _addr(gw), _addr(gb), _addr(ws), wsb,
-                                           L.raw))
-    L.done(x, weight, gy, bias, gate)
+                                           p_gy, _addr(gx), _addr(gg), _addr(gw), _addr(gb), _addr(ws), wsb,
+                                           raw))
+    if other is not None:
+        other.done(x, weight, gy, bias, gate)
     return gx, gw, gb, gg
 
 

@@ -124,7 +124,7 @@ def test_binding_refuses():
         rw.rwkv_selective_scan_forward(x, x, x, x, w)
     with pytest.raises(ValueError, match="CUDA"):
         rw.rwkv_layer_norm_forward(x, w)
-    rows = lambda t, shape=None: rw._rows("t", t, t.shape if shape is None else shape, torch.float32, t.device)
+    rows = lambda t, shape=None: rw._rows("t", t, t.shape if shape is None else shape, torch.float32, -1)
     wide = torch.zeros(3, 4, 20)
     assert rows(wide) == 20 and rows(wide[..., 3:11]) == 20 and rows(wide[:, :1, :8]) == 80
     assert rows(wide[:1, :1, 2:4]) == 2 and rows(torch.zeros(0, 4, 6)) == 6 and rows(wide[..., :1]) == 20
@@ -140,8 +140,8 @@ def test_binding_refuses():
     with pytest.raises(ValueError, match="shape"):
         rows(wide, (3, 4, 21))
     with pytest.raises(ValueError, match="contiguous"):
-        rw._dense("t", wide[..., :8], (3, 4, 8), torch.float32, wide.device)
+        rw._dense("t", wide[..., :8], (3, 4, 8), torch.float32, -1)
     with pytest.raises(ValueError, match="groups"):
-        rw._norm_args(x, torch.zeros(8), None, None, 3)
+        rw._norm_args(x, torch.zeros(8), None, None, 3, -1)
     with pytest.raises(TypeError):
         rw._io_code("x", x.half())
