@@ -17,8 +17,7 @@
 // CTA's accesses are contiguous.  Column sums go to the workspace per team and are added in order
 // by a second kernel: no atomics, the same inputs give the same bits.  Groups wider than 1024
 // vectors take a kernel that reads the row again for each sum (from L1 / L2).  Rows are fetched a turn
-// ahead.  Measured: gated heads 16384x40x64 bf16 46 us forward (5.5 TB/s, 85 % of a copy's rate),
-// 83 + 8 us backward (5.1 TB/s); fp32 8192x768 9.7 us and 16 + 6 us.
+// ahead.  Measured figures stand with the launch.
 #include <algorithm>
 
 #include "launch.h"
@@ -28,11 +27,11 @@ namespace rwkv {
 namespace {
 
 constexpr int kMaxTeam = 512;
-// Threads a launch aims at: enough for two turns of CTAs.  Half of that for the backward's wide teams,
-// whose column sums, one set per team, are large beside the rows a team takes (fp32 8192 x 768: 18.2 +
-// 10.3 us of reduction with the full number, 19.5 + 7.0 with half; 16384 x 40 heads of 64 in bf16: 82
-// against 94 us, so narrow teams keep the full number).
-constexpr int kFillThreads = 148 * 1536;
+// Rows are dealt out to as many teams as fit on the GPU at once: CTAs of a second turn would find
+// their SMs half idle (gated heads 16384x40x64 bf16: 45 us forward, 53 with one and a half turns).  The
+// backward's kernels hold 80 to 128 registers a thread, so 512 threads an SM; each of its teams' column
+// sums cost a pass besides (83 + 8 us with three turns, 78 + 6 with one; fp32 8192x768 16 + 6, 13.6 + 4.8).
+constexpr int kSMs = 148, kBwdThreads = kSMs * 512;
 
 template <int TS>
 constexpr int kCtaThreads = TS > 256 ? TS : 256;
@@ -472,19 +471,39 @@ TeamShape team_shape(int nv) {
   return {0, 0};
 }
 
+// Sets of rows (slices), one per team of a group, for `teams` teams; `min_rows` rows or more each.
+int slices_for(long long M, int G, long long teams, int min_rows) {
+  return (int)std::max<long long>(1, std::min<long long>(teams / G, (M + min_rows - 1) / min_rows));
+}
+
+// CTAs of a kernel that the GPU holds at once; asked once per kernel (`known`).
+int resident_ctas(const void* kernel, int threads, int* known) {
+  int n = __atomic_load_n(known, __ATOMIC_RELAXED);
+  if (n == 0) {
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, 0) != cudaSuccess || n < 1) n = 1;
+    __atomic_store_n(known, n, __ATOMIC_RELAXED);
+  }
+  return n * kSMs;
+}
+
 template <bool BWD, typename T, int V, int K, int TS>
-cudaError_t run_team(const NormParams& p, cudaStream_t st) {
+cudaError_t run_team(NormParams p, cudaStream_t st) {
+  const bool gate = p.gate != nullptr;
+  const auto kernel = BWD ? (gate ? norm_bwd_kernel<T, V, K, TS, true> : norm_bwd_kernel<T, V, K, TS, false>)
+                          : (gate ? norm_fwd_kernel<T, V, K, TS, true> : norm_fwd_kernel<T, V, K, TS, false>);
+  if (!BWD) {
+    static int known[2] = {0, 0};
+    const int ctas = resident_ctas(reinterpret_cast<const void*>(kernel), kCtaThreads<TS>, &known[gate]);
+    p.slices = slices_for(p.M, p.G, (long long)ctas * kTeams<TS>, 1);
+  }
   const long long teams = (long long)p.slices * p.G;
   const unsigned grid = (unsigned)((teams + kTeams<TS> - 1) / kTeams<TS>);
-  const auto kernel =
-      BWD ? (p.gate != nullptr ? norm_bwd_kernel<T, V, K, TS, true> : norm_bwd_kernel<T, V, K, TS, false>)
-          : (p.gate != nullptr ? norm_fwd_kernel<T, V, K, TS, true> : norm_fwd_kernel<T, V, K, TS, false>);
   kernel<<<grid, kCtaThreads<TS>, 0, st>>>(p);
   return cudaGetLastError();
 }
 
 template <bool BWD, typename T, int V>
-cudaError_t run_v(const NormParams& p, cudaStream_t st) {
+cudaError_t run_v(NormParams p, cudaStream_t st) {
   const TeamShape s = team_shape(p.N / V);
   switch (s.ts * 4 + s.k) {
     case 8 * 4 + 1: return run_team<BWD, T, V, 1, 8>(p, st);
@@ -497,6 +516,7 @@ cudaError_t run_v(const NormParams& p, cudaStream_t st) {
     case 512 * 4 + 1: return run_team<BWD, T, V, 1, 512>(p, st);
     case 512 * 4 + 2: return run_team<BWD, T, V, 2, 512>(p, st);
   }
+  if (!BWD) p.slices = slices_for(p.M, p.G, 4 * kSMs, 1);  // wide rows: 4 CTAs of 512 threads an SM
   const unsigned grid = (unsigned)((long long)p.slices * p.G);
   if constexpr (BWD)
     norm_bwd_wide_kernel<T><<<grid, kMaxTeam, 0, st>>>(p);
@@ -511,12 +531,9 @@ cudaError_t run(bool bf16, bool vec, const NormParams& p, cudaStream_t st) {
   return vec ? run_v<BWD, float, 4>(p, st) : run_v<BWD, float, 1>(p, st);
 }
 
-// Sets of rows (slices) that give about kFillThreads threads; 4 rows or more each in the backward.
-int slices_for(long long M, int G, int N, bool vec, bool bf16, bool bwd) {
-  const int ts0 = team_shape(N / (vec ? (bf16 ? 8 : 4) : 1)).ts, ts = ts0 == 0 ? kMaxTeam : ts0;
-  const long long want = std::max<long long>(1, (bwd && ts > 32 ? kFillThreads / 2 : kFillThreads) / ((long long)ts * G));
-  const int min_rows = bwd ? 4 : 1;
-  return (int)std::max<long long>(1, std::min<long long>(want, (M + min_rows - 1) / min_rows));
+int bwd_slices(long long M, int G, int nv) {
+  const int ts = team_shape(nv).ts;
+  return slices_for(M, G, kBwdThreads / (ts == 0 ? kMaxTeam : ts), 4);
 }
 
 }  // namespace
@@ -534,20 +551,18 @@ int parts_for(int slices, int G, int nv) {
 // pointers.
 int norm_bwd_parts(long long M, int G, int N, bool bf16) {
   const int v = bf16 ? 8 : 4;
-  int n = parts_for(slices_for(M, G, N, false, bf16, true), G, N);
-  if (N % v == 0) n = std::max(n, parts_for(slices_for(M, G, N, true, bf16, true), G, N / v));
+  int n = parts_for(bwd_slices(M, G, N), G, N);
+  if (N % v == 0) n = std::max(n, parts_for(bwd_slices(M, G, N / v), G, N / v));
   return n;
 }
 
-cudaError_t launch_norm_fwd(bool bf16, bool vec, const NormParams& p0, cudaStream_t st) {
-  NormParams p = p0;
-  p.slices = slices_for(p.M, p.G, p.N, vec, bf16, false);
+cudaError_t launch_norm_fwd(bool bf16, bool vec, const NormParams& p, cudaStream_t st) {
   return run<false>(bf16, vec, p, st);
 }
 
 cudaError_t launch_norm_bwd(bool bf16, bool vec, const NormParams& p0, cudaStream_t st) {
   NormParams p = p0;
-  p.slices = slices_for(p.M, p.G, p.N, vec, bf16, true);
+  p.slices = bwd_slices(p.M, p.G, vec ? p.N / (bf16 ? 8 : 4) : p.N);
   const cudaError_t e = run<true>(bf16, vec, p, st);
   if (e != cudaSuccess) return e;
   const int C = p.G * p.N;

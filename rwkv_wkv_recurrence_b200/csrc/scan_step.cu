@@ -55,12 +55,17 @@ __global__ void __launch_bounds__(kThreads) scan_step_kernel(const __grid_consta
   for (int b0 = blockIdx.y * kGroup; b0 < p.B; b0 += step) {
     cur = nx;
     if (b0 + step < p.B) fetch(b0 + step);
+    float2 delta[(kGroup + 1) / 2];  // in pairs of streams
+#pragma unroll
+    for (int k = 0; k < kGroup; k += 2) {
+      const int o = k + 1 < kGroup ? k + 1 : k;
+      float2 e;
+      delta[k / 2] = softplus2(make_float2(cur.dt[k][0] + bias, cur.dt[o][0] + bias), e);
+    }
 #pragma unroll
     for (int k = 0; k < kGroup; ++k) {
-      const float x = cur.x[k][0];
-      float2 e;
-      const float delta = softplus2(dup2(cur.dt[k][0] + bias), e).x;
-      const float2 dl = dup2(delta), dx = dup2(delta * x);
+      const float x = cur.x[k][0], dlt = k & 1 ? delta[k / 2].y : delta[k / 2].x;
+      const float2 dl = dup2(dlt), dx = dup2(dlt * x);
       float2 h[2], acc = dup2(0.f);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
