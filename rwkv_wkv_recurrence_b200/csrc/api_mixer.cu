@@ -509,6 +509,17 @@ static rwkv_status norm_check(int64_t M, int64_t G, int64_t N, rwkv_dtype dtype,
   return RWKV_OK;
 }
 
+// `acts`: the activations; absent ones (null) count as lying like x.
+static NormAccess norm_access(int64_t N, size_t esz, const void* x, std::initializer_list<const void*> acts,
+                              std::initializer_list<const float*> params) {
+  const auto at = [](const void* q) { return reinterpret_cast<uintptr_t>(q) % 16; };
+  bool alike = true, on_grid = at(x) == 0 && N % (int64_t)(16 / esz) == 0;
+  for (const void* q : acts) alike = alike && (q == nullptr || at(q) == at(x));
+  for (const float* q : params) on_grid = on_grid && at(q) == 0;
+  if (!alike || N < (int64_t)(16 / esz)) return NormAccess::kSingle;
+  return on_grid ? NormAccess::kAligned : NormAccess::kShifted;
+}
+
 size_t rwkv_layer_norm_backward_workspace_bytes(int64_t M, int64_t G, int64_t N, rwkv_dtype dtype) {
   if (M <= 0 || G <= 0 || N <= 0 || !fits_int(G) || !fits_int(N) || !dtype_ok(dtype) || G * N > INT_MAX / 2) return 0;
   return (size_t)norm_bwd_parts(M, (int)G, (int)N, dtype == RWKV_BF16) * 2 * G * N * sizeof(float);
@@ -535,9 +546,9 @@ rwkv_status rwkv_layer_norm_forward(int64_t M, int64_t G, int64_t N, rwkv_dtype 
   p.x = x;
   p.gate = gate;
   p.y = y;
-  const bool vec = aligned(16, {x, gate, y, weight, bias}) && N % (16 / (int)esz) == 0;
-  return launch_norm_fwd(bf16, vec, p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? RWKV_OK
-                                                                                             : RWKV_ERR_CUDA;
+  const NormAccess access = norm_access(N, esz, x, {gate, y}, {weight, bias});
+  return launch_norm_fwd(bf16, access, p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? RWKV_OK
+                                                                                                : RWKV_ERR_CUDA;
 }
 
 rwkv_status rwkv_layer_norm_backward(int64_t M, int64_t G, int64_t N, rwkv_dtype dtype, const float* weight,
@@ -580,8 +591,8 @@ rwkv_status rwkv_layer_norm_backward(int64_t M, int64_t G, int64_t N, rwkv_dtype
   p.gweight = gweight;
   p.gbias = gbias;
   p.part = static_cast<float*>(workspace);
-  const bool vec = aligned(16, {x, gate, gy, gx, ggate, weight, bias}) && N % (16 / (int)esz) == 0;
-  return launch_norm_bwd(bf16, vec, p, st) == cudaSuccess ? RWKV_OK : RWKV_ERR_CUDA;
+  const NormAccess access = norm_access(N, esz, x, {gate, gy, gx, ggate}, {weight, bias});
+  return launch_norm_bwd(bf16, access, p, st) == cudaSuccess ? RWKV_OK : RWKV_ERR_CUDA;
 }
 
 }  // extern "C"

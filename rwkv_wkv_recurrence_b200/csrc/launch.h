@@ -311,9 +311,12 @@ struct NormParams {
   float* part;          // [norm_bwd_parts()][2][G,N] workspace
   int slices;           // sets of rows whose weight gradients are summed apart
 };
+// kAligned: N and every base allow 16-byte accesses.  kShifted: the activations' bases lie alike on the
+// 16-byte grid and N is a vector or more.  kSingle: any.
+enum class NormAccess { kAligned, kShifted, kSingle };
 int norm_bwd_parts(long long M, int G, int N, bool bf16);
-cudaError_t launch_norm_fwd(bool bf16, bool vec, const NormParams& p, cudaStream_t st);
-cudaError_t launch_norm_bwd(bool bf16, bool vec, const NormParams& p, cudaStream_t st);
+cudaError_t launch_norm_fwd(bool bf16, NormAccess access, const NormParams& p, cudaStream_t st);
+cudaError_t launch_norm_bwd(bool bf16, NormAccess access, const NormParams& p, cudaStream_t st);
 
 // Tensor map over an fp32 [B, T, W] tensor with [1, 64, 32] boxes and the 128-byte swizzle.
 bool make_f32_box32_map(CUtensorMap* m, const void* base, int B, int T, int W);

@@ -142,6 +142,29 @@ struct Raw {
 #pragma unroll
     for (int i = 0; i < (kBytes + 3) / 4; ++i) w[i] = 0u;
   }
+  // Elements lo .. hi - 1 of the V at p (the rest zero), one by one.
+  __device__ __forceinline__ void load_range(const T* p, int lo, int hi) {
+    zero();
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      if (i < lo || i >= hi) continue;
+      if constexpr (sizeof(T) == 4)
+        w[i] = reinterpret_cast<const uint32_t*>(p)[i];
+      else
+        w[i / 2] |= (uint32_t) reinterpret_cast<const unsigned short*>(p)[i] << (16 * (i & 1));
+    }
+  }
+  // Zero outside elements lo .. hi - 1.
+  __device__ __forceinline__ void keep_range(int lo, int hi) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      if (i >= lo && i < hi) continue;
+      if constexpr (sizeof(T) == 4)
+        w[i] = 0u;
+      else
+        w[i / 2] &= (i & 1) != 0 ? 0xFFFFu : 0xFFFF0000u;
+    }
+  }
   // Elements 2 i and 2 i + 1 (0 behind the last).
   __device__ __forceinline__ float2 pair(int i) const {
     return make_float2((*this)[2 * i], 2 * i + 1 < V ? (*this)[2 * i + 1] : 0.f);

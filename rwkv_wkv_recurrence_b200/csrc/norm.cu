@@ -11,13 +11,18 @@
 // would save no pass over the data.
 //
 // One pass over the data, so bandwidth bounds it.  A team of 8 to 512 threads holds one group of a
-// row in registers (1 to 3 vectors a thread): the variance is the mean of (x - mean)², not a
+// row in registers (1 to 4 vectors a thread): the variance is the mean of (x - mean)², not a
 // difference of large sums.  A team keeps its group and strides over the rows, so w and b, and the
 // backward's column sums, stay in registers; teams of neighbouring groups are neighbours, so a
 // CTA's accesses are contiguous.  Column sums go to the workspace per team and are added in order
-// by a second kernel: no atomics, the same inputs give the same bits.  Groups wider than 1024
-// vectors take a kernel that reads the row again for each sum (from L1 / L2).  Rows are fetched a turn
-// ahead.  Measured figures stand with the launch.
+// by a second kernel: no atomics, the same inputs give the same bits.  Groups wider than 1024 vectors
+// (2048 in fp32) take a kernel that reads the row again for each sum (from L1 / L2).  Rows are fetched a
+// turn ahead.  Gated heads 16384x40x64 bf16: 43.6 us forward (5.8 TB/s), 78 and 6 for the column sums
+// backward (5.4 TB/s); fp32 8192x768: 9.2, 13.6 and 4.8.
+//
+// Rows of any length.  Where rows do not start on 16-byte boundaries a team's vectors are laid on those
+// boundaries all the same and the row's first and last vector masked (Cols): 8192x767 fp32 11 us and 24
+// backward, 34 and 64 with single accesses; 16384x2047 bf16 41 and 116, 126 and 581.
 #include <algorithm>
 
 #include "launch.h"
@@ -29,7 +34,7 @@ namespace {
 constexpr int kMaxTeam = 512;
 // Rows are dealt out to as many teams as fit on the GPU at once: CTAs of a second turn would find
 // their SMs half idle (gated heads 16384x40x64 bf16: 45 us forward, 53 with one and a half turns).  The
-// backward's kernels hold 80 to 128 registers a thread, so 512 threads an SM; each of its teams' column
+// backward's kernels mostly hold 80 to 128 registers a thread, so 512 threads an SM; each of its teams' column
 // sums cost a pass besides (83 + 8 us with three turns, 78 + 6 with one; fp32 8192x768 16 + 6, 13.6 + 4.8).
 constexpr int kSMs = 148, kBwdThreads = kSMs * 512;
 
@@ -94,40 +99,93 @@ struct Team {
   }
 };
 
-// A lane's part of a row as loaded: vectors k = 0 .. K-1 at columns (k TS + lane) V; those past
-// column N stay zero.
-template <typename T, int V, int K, int TS>
+// A lane's columns: vectors k = 0 .. K-1 of V columns from c(k) = (k TS + lane) V on.  SHIFT: rows need not
+// start on a vector's boundary in memory; c(k) lies `shift` columns further left, so that every vector is
+// aligned, and the first and the last of a row are shared with its neighbours (`part`).  The launch deals
+// out rows so that all rows of a team have the same shift: parameters and column sums stay in place.
+template <typename T, int V, int K, int TS, bool SHIFT>
+struct Cols {
+  static constexpr bool kShift = SHIFT;
+  int c0, N;
+  bool in[K], part[K];
+  __device__ __forceinline__ Cols(const Team<TS>& tm, const NormParams& p) {
+    N = p.N;
+    c0 = tm.lane * V;
+    if constexpr (SHIFT) {
+      const size_t start = ((size_t)(tm.m < p.M ? tm.m : 0) * p.G + tm.g) * p.N;
+      c0 -= (int)((reinterpret_cast<uintptr_t>(p.x) / sizeof(T) + start) % V);
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      in[k] = c(k) < N;
+      part[k] = SHIFT && in[k] && (c(k) < 0 || c(k) + V > N);
+    }
+  }
+  __device__ __forceinline__ int c(int k) const { return c0 + k * TS * V; }
+  __device__ __forceinline__ bool has(int k, int i) const { return (unsigned)(c(k) + i) < (unsigned)N; }
+};
+
+// A lane's part of a row as loaded; what lies past column N (in `part` vectors before column 0 too) is
+// zero after mask().
+template <typename T, int V, int K, int TS, bool SHIFT>
 struct RowPart {
+  using C = Cols<T, V, K, TS, SHIFT>;
   Raw<T, V> v[K];
   __device__ __forceinline__ void zero() {
 #pragma unroll
     for (int k = 0; k < K; ++k) v[k].zero();
   }
-  __device__ __forceinline__ void load(const T* lane0, const bool (&in)[K]) {  // lane0: the lane's first column
+  // lane0: the lane's first column.  `inner`: there is a row before and one behind, so shared vectors
+  // may be read whole.
+  __device__ __forceinline__ void load(const T* lane0, const C& cols, bool inner) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if (!cols.in[k]) continue;
+      if (!cols.part[k] || inner)
+        v[k].load(lane0 + k * TS * V);
+      else
+        v[k].load_range(lane0 + k * TS * V, -cols.c(k), cols.N - cols.c(k));
+    }
+  }
+  __device__ __forceinline__ void mask(const C& cols) {
 #pragma unroll
     for (int k = 0; k < K; ++k)
-      if (in[k]) v[k].load(lane0 + k * TS * V);
+      if (cols.part[k]) v[k].keep_range(-cols.c(k), cols.N - cols.c(k));
   }
 };
 
-// Parameters of a group in the same places, in pairs (with V = 1 a pair's second half is idle).
-template <int V, int K, int TS>
-__device__ __forceinline__ void load_params(const float* row, int lane, const bool (&in)[K],
-                                            float2 (&f)[K][(V + 1) / 2]) {
+// Parameters of a group in a vector's places, in pairs (with V = 1 a pair's second half is idle).
+template <int V, typename C>
+__device__ __forceinline__ void load_params(const float* row, const C& cols, int k, float2 (&f)[(V + 1) / 2]) {
+  Raw<float, V> r;
+  r.zero();
+  if (row != nullptr && cols.in[k]) {
+    if constexpr (C::kShift)
+      r.load_range(row + cols.c(k), -cols.c(k), cols.N - cols.c(k));
+    else
+      r.load(row + cols.c(k));
+  }
 #pragma unroll
-  for (int k = 0; k < K; ++k) {
-    Raw<float, V> r;
-    r.zero();
-    if (row != nullptr && in[k]) r.load(row + (k * TS + lane) * V);
+  for (int i = 0; i < (V + 1) / 2; ++i) f[i] = r.pair(i);
+}
+
+// A vector's results, of a shared vector only the row's own.
+template <typename T, int V, typename C>
+__device__ __forceinline__ void store_cols(T* at, const C& cols, int k, const float2 (&o)[(V + 1) / 2]) {
+  if (!C::kShift || !cols.part[k]) {
+    store_pairs_as<T, V>(at, o);
+  } else {
 #pragma unroll
-    for (int i = 0; i < (V + 1) / 2; ++i) f[k][i] = r.pair(i);
+    for (int i = 0; i < V; ++i)
+      if (cols.has(k, i)) at[i] = IO<T>::from_f(i & 1 ? o[i / 2].y : o[i / 2].x);
   }
 }
 
-// x - mean (0 past column N); returns 1 / sqrt(var + eps).
-template <typename T, int V, int K, int TS>
-__device__ __forceinline__ float center(const RowPart<T, V, K, TS>& r, float2 (&x)[K][(V + 1) / 2],
-                                        const bool (&in)[K], float inv_n, float eps, TeamSum<TS>& sum) {
+// x - mean (0 outside the row); returns 1 / sqrt(var + eps).
+template <typename T, int V, int K, int TS, bool SHIFT>
+__device__ __forceinline__ float center(const RowPart<T, V, K, TS, SHIFT>& r, float2 (&x)[K][(V + 1) / 2],
+                                        const Cols<T, V, K, TS, SHIFT>& cols, float inv_n, float eps,
+                                        TeamSum<TS>& sum) {
   constexpr int P = (V + 1) / 2;
   float2 s = dup2(0.f);
 #pragma unroll
@@ -138,62 +196,72 @@ __device__ __forceinline__ float center(const RowPart<T, V, K, TS>& r, float2 (&
   float2 q = dup2(0.f);
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    const float mk = in[k] ? -mean : 0.f;
+    const float mk = cols.in[k] ? -mean : 0.f;
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-      x[k][i] = add2(x[k][i], make_float2(mk, V == 1 ? 0.f : mk));
-      q = fma2(x[k][i], x[k][i], q);
+    for (int i = 0; i < P; ++i) x[k][i] = add2(x[k][i], make_float2(mk, V == 1 ? 0.f : mk));
+    if (cols.part[k]) {
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        if (!cols.has(k, 2 * i)) x[k][i].x = 0.f;
+        if (!cols.has(k, 2 * i + 1)) x[k][i].y = 0.f;
+      }
     }
+#pragma unroll
+    for (int i = 0; i < P; ++i) q = fma2(x[k][i], x[k][i], q);
   }
   return rsqrtf(fmaf(sum(q.x + q.y), inv_n, eps));
 }
 
 // Rows are fetched a turn ahead and left as loaded until they are due; behind the last row the last
 // fetch is repeated and not used.
-template <typename T, int V, int K, int TS, bool GATE>
+template <typename T, int V, int K, int TS, bool GATE, bool SHIFT>
 __global__ void __launch_bounds__(kCtaThreads<TS>) norm_fwd_kernel(const __grid_constant__ NormParams p) {
   constexpr int P = (V + 1) / 2;
   __shared__ float2 buf[TeamSum<TS>::kBuf];
   TeamSum<TS> sum{buf};
   const Team<TS> tm(p);
   const float inv_n = 1.f / (float)p.N;
-  bool in[K];
-#pragma unroll
-  for (int k = 0; k < K; ++k) in[k] = (k * TS + tm.lane) * V < p.N;
+  const Cols<T, V, K, TS, SHIFT> cols(tm, p);
   const ptrdiff_t stride = (ptrdiff_t)tm.step * p.G * p.N;
-  const size_t off = ((size_t)(tm.m < p.M ? tm.m : 0) * p.G + tm.g) * p.N + tm.lane * V;
+  const ptrdiff_t off = ((ptrdiff_t)(tm.m < p.M ? tm.m : 0) * p.G + tm.g) * p.N + cols.c0;
   const T* x_at = static_cast<const T*>(p.x) + off;
   const T* z_at = GATE ? static_cast<const T*>(p.gate) + off : nullptr;
   T* y_at = static_cast<T*>(p.y) + off;
   long long m = tm.m;
-  RowPart<T, V, K, TS> rx, rz;
+  const long long last = p.M - 1;
+  const bool inner = m > 0 && m < last;
+  RowPart<T, V, K, TS, SHIFT> rx, rz;
   rx.zero();
-  rx.load(x_at, in);
+  rx.load(x_at, cols, inner);
   if constexpr (GATE) {
     rz.zero();
-    rz.load(z_at, in);
+    rz.load(z_at, cols, inner);
   }
   float2 w[K][P], b[K][P];
-  load_params<V, K, TS>(p.weight + (size_t)tm.g * p.N, tm.lane, in, w);
-  load_params<V, K, TS>(p.bias != nullptr ? p.bias + (size_t)tm.g * p.N : nullptr, tm.lane, in, b);
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    load_params<V>(p.weight + (size_t)tm.g * p.N, cols, k, w[k]);
+    load_params<V>(p.bias != nullptr ? p.bias + (size_t)tm.g * p.N : nullptr, cols, k, b[k]);
+  }
   for (long long it = 0; it < tm.turns; ++it) {
     const bool on = m < p.M;
-    const RowPart<T, V, K, TS> cx = rx, cz = rz;
+    RowPart<T, V, K, TS, SHIFT> cx = rx, cz = rz;
     m += tm.step;
     if (m < p.M) {
       x_at += stride;
-      rx.load(x_at, in);
+      rx.load(x_at, cols, m < last);
       if constexpr (GATE) {
         z_at += stride;
-        rz.load(z_at, in);
+        rz.load(z_at, cols, m < last);
       }
     }
+    cx.mask(cols);  // of the gate only the row's own columns are used
     float2 x[K][P];
-    const float2 rstd = dup2(center<T, V, K, TS>(cx, x, in, inv_n, p.eps, sum));
+    const float2 rstd = dup2(center<T, V, K, TS, SHIFT>(cx, x, cols, inv_n, p.eps, sum));
     if (on) {
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        if (!in[k]) continue;
+        if (!cols.in[k]) continue;
         float2 o[P];
 #pragma unroll
         for (int i = 0; i < P; ++i) {
@@ -203,64 +271,69 @@ __global__ void __launch_bounds__(kCtaThreads<TS>) norm_fwd_kernel(const __grid_
             o[i] = mul2(o[i], mul2(z, sigmoid2(z)));
           }
         }
-        store_pairs_as<T, V>(y_at + k * TS * V, o);
+        store_cols<T, V>(y_at + k * TS * V, cols, k, o);
       }
     }
     y_at += stride;
   }
 }
 
-template <typename T, int V, int K, int TS, bool GATE>
+template <typename T, int V, int K, int TS, bool GATE, bool SHIFT>
 __global__ void __launch_bounds__(kCtaThreads<TS>) norm_bwd_kernel(const __grid_constant__ NormParams p) {
   constexpr int P = (V + 1) / 2;
   __shared__ float2 buf[TeamSum<TS>::kBuf];
   TeamSum<TS> sum{buf};
   const Team<TS> tm(p);
   const float inv_n = 1.f / (float)p.N;
-  bool in[K];
-#pragma unroll
-  for (int k = 0; k < K; ++k) in[k] = (k * TS + tm.lane) * V < p.N;
+  const Cols<T, V, K, TS, SHIFT> cols(tm, p);
   const ptrdiff_t stride = (ptrdiff_t)tm.step * p.G * p.N;
-  const size_t off = ((size_t)(tm.m < p.M ? tm.m : 0) * p.G + tm.g) * p.N + tm.lane * V;
+  const ptrdiff_t off = ((ptrdiff_t)(tm.m < p.M ? tm.m : 0) * p.G + tm.g) * p.N + cols.c0;
   const T* x_at = static_cast<const T*>(p.x) + off;
   const T* g_at = static_cast<const T*>(p.gy) + off;
   const T* z_at = GATE ? static_cast<const T*>(p.gate) + off : nullptr;
   T* gx_at = static_cast<T*>(p.gx) + off;
   T* gz_at = GATE ? static_cast<T*>(p.ggate) + off : nullptr;
   long long m = tm.m;
-  RowPart<T, V, K, TS> rx, rg, rz;
+  const long long last = p.M - 1;
+  const bool inner = m > 0 && m < last;
+  RowPart<T, V, K, TS, SHIFT> rx, rg, rz;
   rx.zero();
-  rx.load(x_at, in);
+  rx.load(x_at, cols, inner);
   rg.zero();
-  rg.load(g_at, in);
+  rg.load(g_at, cols, inner);
   if constexpr (GATE) {
     rz.zero();
-    rz.load(z_at, in);
+    rz.load(z_at, cols, inner);
   }
   float2 w[K][P], b[K][P], gw[K][P], gb[K][P];
-  load_params<V, K, TS>(p.weight + (size_t)tm.g * p.N, tm.lane, in, w);
-  if constexpr (GATE)
-    load_params<V, K, TS>(p.bias != nullptr ? p.bias + (size_t)tm.g * p.N : nullptr, tm.lane, in, b);
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    load_params<V>(p.weight + (size_t)tm.g * p.N, cols, k, w[k]);
+    if constexpr (GATE) load_params<V>(p.bias != nullptr ? p.bias + (size_t)tm.g * p.N : nullptr, cols, k, b[k]);
+  }
 #pragma unroll
   for (int k = 0; k < K; ++k)
 #pragma unroll
     for (int i = 0; i < P; ++i) gw[k][i] = gb[k][i] = dup2(0.f);
   for (long long it = 0; it < tm.turns; ++it) {
     const bool on = m < p.M;
-    const RowPart<T, V, K, TS> cx = rx, cg = rg, cz = rz;
+    RowPart<T, V, K, TS, SHIFT> cx = rx, cg = rg, cz = rz;
     m += tm.step;
     if (m < p.M) {
       x_at += stride;
       g_at += stride;
-      rx.load(x_at, in);
-      rg.load(g_at, in);
+      rx.load(x_at, cols, m < last);
+      rg.load(g_at, cols, m < last);
       if constexpr (GATE) {
         z_at += stride;
-        rz.load(z_at, in);
+        rz.load(z_at, cols, m < last);
       }
     }
+    cx.mask(cols);
+    cg.mask(cols);
+    if constexpr (GATE) cz.mask(cols);
     float2 x[K][P], u[K][P], z[K][P];
-    const float rstd = center<T, V, K, TS>(cx, x, in, inv_n, p.eps, sum);
+    const float rstd = center<T, V, K, TS, SHIFT>(cx, x, cols, inv_n, p.eps, sum);
     float2 su = dup2(0.f), sx = dup2(0.f);
 #pragma unroll
     for (int k = 0; k < K; ++k)
@@ -287,12 +360,12 @@ __global__ void __launch_bounds__(kCtaThreads<TS>) norm_bwd_kernel(const __grid_
       const float2 c0 = dup2(-rstd * r.x * inv_n), c1 = dup2(-rstd * r.y * inv_n);
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        if (!in[k]) continue;
+        if (!cols.in[k]) continue;
         float2 o[P];
 #pragma unroll
         for (int i = 0; i < P; ++i) o[i] = fma2(dup2(rstd), u[k][i], fma2(c1, x[k][i], c0));
-        store_pairs_as<T, V>(gx_at + k * TS * V, o);
-        if constexpr (GATE) store_pairs_as<T, V>(gz_at + k * TS * V, z[k]);
+        store_cols<T, V>(gx_at + k * TS * V, cols, k, o);
+        if constexpr (GATE) store_cols<T, V>(gz_at + k * TS * V, cols, k, z[k]);
       }
     }
     gx_at += stride;
@@ -303,7 +376,7 @@ __global__ void __launch_bounds__(kCtaThreads<TS>) norm_bwd_kernel(const __grid_
   long long part_id = ((long long)blockIdx.x * kTeams<TS> + threadIdx.x / TS) / p.G;
   bool write = part_id < p.slices;
   if constexpr (kTeams<TS> > 1) {
-    __shared__ float2 acc[2][K * TS * P];
+    __shared__ float2 acc[2][K * TS * P];  // SHIFT: by column, as its teams' columns lie differently
     if (p.G == 1) {
       const int team = threadIdx.x / TS;
       for (int t = 0; t < kTeams<TS>; ++t) {
@@ -312,10 +385,23 @@ __global__ void __launch_bounds__(kCtaThreads<TS>) norm_bwd_kernel(const __grid_
           for (int k = 0; k < K; ++k)
 #pragma unroll
             for (int i = 0; i < P; ++i) {
-              float2& a = acc[0][(k * P + i) * TS + tm.lane];
-              float2& c = acc[1][(k * P + i) * TS + tm.lane];
-              if (t > 0) gw[k][i] = add2(a, gw[k][i]), gb[k][i] = add2(c, gb[k][i]);
-              a = gw[k][i], c = gb[k][i];
+              if constexpr (SHIFT) {
+                float* a = &acc[0][0].x + cols.c(k) + 2 * i;
+                float* c = &acc[1][0].x + cols.c(k) + 2 * i;
+                if (cols.has(k, 2 * i)) {
+                  if (t > 0) gw[k][i].x += a[0], gb[k][i].x += c[0];
+                  a[0] = gw[k][i].x, c[0] = gb[k][i].x;
+                }
+                if (cols.has(k, 2 * i + 1)) {
+                  if (t > 0) gw[k][i].y += a[1], gb[k][i].y += c[1];
+                  a[1] = gw[k][i].y, c[1] = gb[k][i].y;
+                }
+              } else {
+                float2& a = acc[0][(k * P + i) * TS + tm.lane];
+                float2& c = acc[1][(k * P + i) * TS + tm.lane];
+                if (t > 0) gw[k][i] = add2(a, gw[k][i]), gb[k][i] = add2(c, gb[k][i]);
+                a = gw[k][i], c = gb[k][i];
+              }
             }
         }
         __syncthreads();
@@ -328,10 +414,18 @@ __global__ void __launch_bounds__(kCtaThreads<TS>) norm_bwd_kernel(const __grid_
   float* part = p.part + (size_t)part_id * 2 * p.G * p.N + (size_t)tm.g * p.N;
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    if (!in[k]) continue;
-    const int col = (k * TS + tm.lane) * V;
-    store_pairs_as<float, V>(part + col, gw[k]);
-    store_pairs_as<float, V>(part + (size_t)p.G * p.N + col, gb[k]);
+    if (!cols.in[k]) continue;
+    if constexpr (SHIFT) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        if (!cols.has(k, i)) continue;
+        part[cols.c(k) + i] = i & 1 ? gw[k][i / 2].y : gw[k][i / 2].x;
+        part[(size_t)p.G * p.N + cols.c(k) + i] = i & 1 ? gb[k][i / 2].y : gb[k][i / 2].x;
+      }
+    } else {
+      store_pairs_as<float, V>(part + cols.c(k), gw[k]);
+      store_pairs_as<float, V>(part + (size_t)p.G * p.N + cols.c(k), gb[k]);
+    }
   }
 }
 
@@ -454,11 +548,16 @@ __global__ void __launch_bounds__(1024) norm_reduce_kernel(int slices, int C, co
   }
 }
 
-// Threads of a team and vectors per thread for nv vectors a group; 0 threads: the wide kernel.
+// Threads of a team and vectors (of v elements) per thread for nv vectors a group; 0 threads: the wide
+// kernel.  Few threads with several vectors meet faster than many with one: 512 x 1 for 4096 columns in
+// bf16 took 72 us forward and 145 backward (16384 rows), 256 x 2 51 and 84; 128 x 3 for 2560 columns 9.6
+// and 22 (4096 rows), 256 x 2 12.7 and 25.  Three and four vectors of 512 threads hold their registers
+// in fp32 only, the gated backward not quite: 4096x6832 gated fp32 54 us and 222, with the wide kernel 177
+// and 553.
 struct TeamShape {
   int ts, k;
 };
-TeamShape team_shape(int nv) {
+TeamShape team_shape(int nv, int v) {
   if (nv <= 8) return {8, 1};
   if (nv <= 16) return {16, 1};
   if (nv <= 32) return {32, 1};
@@ -466,10 +565,17 @@ TeamShape team_shape(int nv) {
   if (nv <= 128) return {64, 2};
   if (nv <= 192) return {64, 3};
   if (nv <= 256) return {128, 2};
-  if (nv <= 512) return {512, 1};
+  if (nv <= 384) return {128, 3};
+  if (nv <= 512) return {256, 2};
+  if (nv <= 768) return {256, 3};
   if (nv <= 1024) return {512, 2};
+  if (nv <= 1536 && v < 8) return {512, 3};
+  if (nv <= 2048 && v < 8) return {512, 4};
   return {0, 0};
 }
+
+// Vectors of a row, at any shift.
+int row_vectors(int N, int V, bool shift) { return (shift ? N + 2 * V - 2 : N) / V; }
 
 // Sets of rows (slices), one per team of a group, for `teams` teams; `min_rows` rows or more each.
 int slices_for(long long M, int G, long long teams, int min_rows) {
@@ -486,15 +592,25 @@ int resident_ctas(const void* kernel, int threads, int* known) {
   return n * kSMs;
 }
 
-template <bool BWD, typename T, int V, int K, int TS>
+// Rows between two of equal shift (a power of two): rows of a team are a multiple of it apart.
+int shift_period(int N, int V) {
+  int q = V;
+  while (q > 1 && N % 2 == 0) q /= 2, N /= 2;
+  return q;
+}
+int whole_periods(int slices, int q) { return std::max(1, slices / q) * q; }
+
+template <bool BWD, typename T, int V, int K, int TS, bool SHIFT>
 cudaError_t run_team(NormParams p, cudaStream_t st) {
   const bool gate = p.gate != nullptr;
-  const auto kernel = BWD ? (gate ? norm_bwd_kernel<T, V, K, TS, true> : norm_bwd_kernel<T, V, K, TS, false>)
-                          : (gate ? norm_fwd_kernel<T, V, K, TS, true> : norm_fwd_kernel<T, V, K, TS, false>);
+  const auto kernel =
+      BWD ? (gate ? norm_bwd_kernel<T, V, K, TS, true, SHIFT> : norm_bwd_kernel<T, V, K, TS, false, SHIFT>)
+          : (gate ? norm_fwd_kernel<T, V, K, TS, true, SHIFT> : norm_fwd_kernel<T, V, K, TS, false, SHIFT>);
   if (!BWD) {
     static int known[2] = {0, 0};
     const int ctas = resident_ctas(reinterpret_cast<const void*>(kernel), kCtaThreads<TS>, &known[gate]);
     p.slices = slices_for(p.M, p.G, (long long)ctas * kTeams<TS>, 1);
+    if (SHIFT) p.slices = whole_periods(p.slices, shift_period(p.N, V));
   }
   const long long teams = (long long)p.slices * p.G;
   const unsigned grid = (unsigned)((teams + kTeams<TS> - 1) / kTeams<TS>);
@@ -502,19 +618,27 @@ cudaError_t run_team(NormParams p, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-template <bool BWD, typename T, int V>
+template <bool BWD, typename T, int V, bool SHIFT>
 cudaError_t run_v(NormParams p, cudaStream_t st) {
-  const TeamShape s = team_shape(p.N / V);
-  switch (s.ts * 4 + s.k) {
-    case 8 * 4 + 1: return run_team<BWD, T, V, 1, 8>(p, st);
-    case 16 * 4 + 1: return run_team<BWD, T, V, 1, 16>(p, st);
-    case 32 * 4 + 1: return run_team<BWD, T, V, 1, 32>(p, st);
-    case 32 * 4 + 2: return run_team<BWD, T, V, 2, 32>(p, st);
-    case 64 * 4 + 2: return run_team<BWD, T, V, 2, 64>(p, st);
-    case 64 * 4 + 3: return run_team<BWD, T, V, 3, 64>(p, st);
-    case 128 * 4 + 2: return run_team<BWD, T, V, 2, 128>(p, st);
-    case 512 * 4 + 1: return run_team<BWD, T, V, 1, 512>(p, st);
-    case 512 * 4 + 2: return run_team<BWD, T, V, 2, 512>(p, st);
+  const TeamShape s = team_shape(row_vectors(p.N, V, SHIFT), V);
+  switch (s.ts * 8 + s.k) {
+    case 8 * 8 + 1: return run_team<BWD, T, V, 1, 8, SHIFT>(p, st);
+    case 16 * 8 + 1: return run_team<BWD, T, V, 1, 16, SHIFT>(p, st);
+    case 32 * 8 + 1: return run_team<BWD, T, V, 1, 32, SHIFT>(p, st);
+    case 32 * 8 + 2: return run_team<BWD, T, V, 2, 32, SHIFT>(p, st);
+    case 64 * 8 + 2: return run_team<BWD, T, V, 2, 64, SHIFT>(p, st);
+    case 64 * 8 + 3: return run_team<BWD, T, V, 3, 64, SHIFT>(p, st);
+    case 128 * 8 + 2: return run_team<BWD, T, V, 2, 128, SHIFT>(p, st);
+    case 128 * 8 + 3: return run_team<BWD, T, V, 3, 128, SHIFT>(p, st);
+    case 256 * 8 + 2: return run_team<BWD, T, V, 2, 256, SHIFT>(p, st);
+    case 256 * 8 + 3: return run_team<BWD, T, V, 3, 256, SHIFT>(p, st);
+    case 512 * 8 + 2: return run_team<BWD, T, V, 2, 512, SHIFT>(p, st);
+    case 512 * 8 + 3:
+      if constexpr (V < 8) return run_team<BWD, T, V, 3, 512, SHIFT>(p, st);
+      break;
+    case 512 * 8 + 4:
+      if constexpr (V < 8) return run_team<BWD, T, V, 4, 512, SHIFT>(p, st);
+      break;
   }
   if (!BWD) p.slices = slices_for(p.M, p.G, 4 * kSMs, 1);  // wide rows: 4 CTAs of 512 threads an SM
   const unsigned grid = (unsigned)((long long)p.slices * p.G);
@@ -525,49 +649,59 @@ cudaError_t run_v(NormParams p, cudaStream_t st) {
   return cudaGetLastError();
 }
 
+template <bool BWD, typename T>
+cudaError_t run_t(NormAccess access, const NormParams& p, cudaStream_t st) {
+  constexpr int V = 16 / (int)sizeof(T);
+  switch (access) {
+    case NormAccess::kAligned: return run_v<BWD, T, V, false>(p, st);
+    case NormAccess::kShifted: return run_v<BWD, T, V, true>(p, st);
+    case NormAccess::kSingle: return run_v<BWD, T, 1, false>(p, st);
+  }
+  return cudaErrorInvalidValue;
+}
+
 template <bool BWD>
-cudaError_t run(bool bf16, bool vec, const NormParams& p, cudaStream_t st) {
-  if (bf16) return vec ? run_v<BWD, __nv_bfloat16, 8>(p, st) : run_v<BWD, __nv_bfloat16, 1>(p, st);
-  return vec ? run_v<BWD, float, 4>(p, st) : run_v<BWD, float, 1>(p, st);
+cudaError_t run(bool bf16, NormAccess access, const NormParams& p, cudaStream_t st) {
+  return bf16 ? run_t<BWD, __nv_bfloat16>(access, p, st) : run_t<BWD, float>(access, p, st);
 }
 
-int bwd_slices(long long M, int G, int nv) {
-  const int ts = team_shape(nv).ts;
-  return slices_for(M, G, kBwdThreads / (ts == 0 ? kMaxTeam : ts), 4);
+// The backward's slices and sets of column sums: a CTA's teams share a set where there is one group.
+struct BwdPlan {
+  int slices, parts;
+};
+BwdPlan bwd_plan(long long M, int G, int N, bool bf16, NormAccess access) {
+  const bool shift = access == NormAccess::kShifted;
+  const int v = access == NormAccess::kSingle ? 1 : (bf16 ? 8 : 4);
+  const int ts = team_shape(row_vectors(N, v, shift), v).ts;
+  const int teams = ts == 0 || ts > 256 ? 1 : 256 / ts;  // a CTA's
+  int slices = slices_for(M, G, kBwdThreads / (ts == 0 ? kMaxTeam : ts), 4);
+  if (shift && ts != 0) slices = whole_periods(slices, shift_period(N, v));
+  return {slices, G == 1 ? (slices + teams - 1) / teams : slices};
 }
 
 }  // namespace
 
-namespace {
-// Sets of column sums that the backward's teams write: a CTA's teams share one where there is one group.
-int parts_for(int slices, int G, int nv) {
-  const int ts = team_shape(nv).ts;
-  const int teams = ts == 0 ? 1 : (ts > 256 ? 1 : 256 / ts);
-  return G == 1 ? (slices + teams - 1) / teams : slices;
-}
-}  // namespace
-
-// Bounds the sets of column sums by sizes alone (aligned or not), so that the workspace query needs no
-// pointers.
+// Bounds the sets of column sums by sizes alone (however the arrays lie), so that the workspace query
+// needs no pointers.
 int norm_bwd_parts(long long M, int G, int N, bool bf16) {
-  const int v = bf16 ? 8 : 4;
-  int n = parts_for(bwd_slices(M, G, N), G, N);
-  if (N % v == 0) n = std::max(n, parts_for(bwd_slices(M, G, N / v), G, N / v));
+  int n = 0;
+  for (const NormAccess a : {NormAccess::kAligned, NormAccess::kShifted, NormAccess::kSingle})
+    if (a != NormAccess::kAligned || N % (bf16 ? 8 : 4) == 0) n = std::max(n, bwd_plan(M, G, N, bf16, a).parts);
   return n;
 }
 
-cudaError_t launch_norm_fwd(bool bf16, bool vec, const NormParams& p, cudaStream_t st) {
-  return run<false>(bf16, vec, p, st);
+cudaError_t launch_norm_fwd(bool bf16, NormAccess access, const NormParams& p, cudaStream_t st) {
+  return run<false>(bf16, access, p, st);
 }
 
-cudaError_t launch_norm_bwd(bool bf16, bool vec, const NormParams& p0, cudaStream_t st) {
+cudaError_t launch_norm_bwd(bool bf16, NormAccess access, const NormParams& p0, cudaStream_t st) {
   NormParams p = p0;
-  p.slices = bwd_slices(p.M, p.G, vec ? p.N / (bf16 ? 8 : 4) : p.N);
-  const cudaError_t e = run<true>(bf16, vec, p, st);
+  const BwdPlan plan = bwd_plan(p.M, p.G, p.N, bf16, access);
+  p.slices = plan.slices;
+  const cudaError_t e = run<true>(bf16, access, p, st);
   if (e != cudaSuccess) return e;
   const int C = p.G * p.N;
-  norm_reduce_kernel<<<(unsigned)((2LL * C + 31) / 32), 1024, 0, st>>>(
-      parts_for(p.slices, p.G, vec ? p.N / (bf16 ? 8 : 4) : p.N), C, p.part, p.gweight, p.gbias);
+  norm_reduce_kernel<<<(unsigned)((2LL * C + 31) / 32), 1024, 0, st>>>(plan.parts, C, p.part, p.gweight, p.gbias);
   return cudaGetLastError();
 }
 

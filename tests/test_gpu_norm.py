@@ -128,3 +128,61 @@ def test_same_bits_twice(cuda_device):
     q = {k: v.to(cuda_device) for k, v in _inputs(3000, 320, 48, torch.bfloat16).items()}
     a, b = _run(q, 5, True, True), _run(q, 5, True, True)
     assert all(torch.equal(a[k], b[k]) for k in a)
+
+
+@DT
+@pytest.mark.parametrize("shape", [(20000, 1, 37), (3001, 40, 67), (1, 1, 333), (2, 3, 9), (7, 2, 4091), (1500, 1, 2050),
+                                   (300, 1, 4100), (64, 5, 1023)], ids=str)
+def test_rows_that_start_anywhere(cuda_device, shape, dtype):
+    # rows share 16-byte vectors with their neighbours; a team's rows all lie alike
+    M, G, N = shape
+    p = _inputs(M, G * N, 49, dtype)
+    q = {k: v.to(cuda_device) for k, v in p.items()}
+    for gate, bias in ((True, True), (False, False)):
+        r = ref.norm(p["x"], p["w"], p["bias"] if bias else None, p["gate"] if gate else None, G, 1e-5, p["gy"])
+        ref.check_all(_run(q, G, gate, bias), r, f"gate={gate} bias={bias} ")
+
+
+@DT
+@pytest.mark.parametrize("N", [33, 77, 600])
+def test_nan_stays_in_its_row_where_vectors_are_shared(cuda_device, N, dtype):
+    p = {k: v.to(cuda_device) for k, v in _inputs(40, 4 * N, 50, dtype).items()}
+    clean = _run(p, 4, True, True)
+    hit = torch.zeros(40, 4 * N, dtype=torch.bool, device=cuda_device)
+    for m in (0, 11, 12, 39):
+        for name in ("x", "gate"):
+            p[name][m, N: 2 * N] = float("nan") if m % 2 else float("inf")
+        hit[m, N: 2 * N] = True
+    got = _run(p, 4, True, True)
+    for k in ("y", "gx", "ggate"):
+        assert not torch.isfinite(got[k][hit]).any() and torch.equal(got[k][~hit], clean[k][~hit]), k
+
+
+@DT
+@pytest.mark.parametrize("G,N", [(3, 33), (1, 264), (2, 64), (1, 1001), (4, 12)])
+@pytest.mark.parametrize("M", [1, 2, 50])
+def test_all_bases_off_the_grid_alike(cuda_device, M, G, N, dtype):
+    C = G * N
+    p = _inputs(M, C, 51, dtype)
+    code = rw.F32 if dtype == torch.float32 else rw.BF16
+    for off in (1, 3):
+        q = {}
+        for k, v in p.items():
+            buf = Guarded(tuple(v.shape), v.dtype, cuda_device, off)  # its surroundings are not the operator's
+            buf.t.copy_(v)
+            q[k] = buf
+        h, P, S = rw.lib(), rw._ptr, rw._stream(None)
+        y, gx, gg = (Guarded((M, C), dtype, cuda_device, off) for _ in range(3))
+        gw, gb = Guarded((C,), torch.float32, cuda_device), Guarded((C,), torch.float32, cuda_device)
+        wsb = int(h.rwkv_layer_norm_backward_workspace_bytes(M, G, N, code))
+        ws = Guarded((wsb // 4,), torch.float32, cuda_device)
+        ptr = lambda k: q[k].ptr()
+        assert h.rwkv_layer_norm_forward(M, G, N, code, ptr("w"), ptr("bias"), 1e-5, ptr("x"), ptr("gate"), y.ptr(),
+                                         S) == 0
+        assert h.rwkv_layer_norm_backward(M, G, N, code, ptr("w"), ptr("bias"), 1e-5, ptr("x"), ptr("gate"), ptr("gy"),
+                                          gx.ptr(), gg.ptr(), gw.ptr(), gb.ptr(), ws.ptr(), wsb, S) == 0
+        rw.rwkv_check_device_error()
+        for b_, name in ((y, "y"), (gx, "gx"), (gg, "ggate"), (gw, "gw"), (gb, "gbias"), (ws, "workspace")):
+            b_.check(name)
+        r = ref.norm(p["x"], p["w"], p["bias"], p["gate"], G, 1e-5, p["gy"])
+        ref.check_all(dict(y=y.t, gx=gx.t, gw=gw.t, gbias=gb.t, ggate=gg.t), r, f"off={off} ")
