@@ -61,21 +61,41 @@ struct Shape {
   }
 };
 
-// A run of elements that a thread fetches into shared memory for itself: pieces of up to 16 bytes,
+// A thread's elements of a tile, as in the forward.  VEC: a run of channels of one token, in wide
+// accesses.  Else one channel of every kStep-th token (4x1024x2561, N = 8, bf16: the backward in 0.36 ms,
+// 0.58 with runs of single accesses, 0.26 for 2560 channels).
+template <typename S, bool VEC>
+struct Place {
+  static constexpr int kStep = kThreads / S::kCh;
+  int t, ch;  // the first element's token in the tile and channel in the CTA
+  __device__ __forceinline__ Place() {
+    const int tid = threadIdx.x;
+    t = VEC ? tid / S::kTokThreads : tid / S::kCh;
+    ch = VEC ? tid % S::kTokThreads * S::kRun : tid % S::kCh;
+  }
+  __device__ __forceinline__ int tok(int i) const { return VEC ? t : t + i * kStep; }
+  __device__ __forceinline__ int chan(int i) const { return VEC ? ch + i : ch; }
+};
+
+// Elements that a thread fetches into shared memory for itself.  VEC: a run in pieces of up to 16 bytes,
 // piece k of thread tid at (k kThreads + tid) pieces.
-template <typename T, int RUN>
+template <typename T, typename S, bool VEC>
 struct Stage {
+  static constexpr int RUN = S::kRun;
+  using Got = Raw<T, RUN>;
   static constexpr int kBytes = RUN * (int)sizeof(T);
   static constexpr int kPiece = kBytes < 16 ? kBytes : 16;
   static constexpr int kElems = kPiece / (int)sizeof(T);
   static constexpr int kPieces = kBytes / kPiece;
   unsigned char raw[kPieces * kThreads * kPiece];
 
-  __device__ __forceinline__ void fetch(const T* src, int n, bool vec) {
+  // src: the first element; left: tokens from there to the segment's end, nc: channels to the last.
+  __device__ __forceinline__ void fetch(const T* src, int64_t, int left, int nc, bool) {
+    const int n = left > 0 ? nc : 0;
 #pragma unroll
     for (int k = 0; k < kPieces; ++k) {
       T* dst = reinterpret_cast<T*>(raw + (k * kThreads + threadIdx.x) * kPiece);
-      if (vec && n >= RUN) {
+      if (n >= RUN) {
         const uint32_t d = smem_u32(dst);
         if constexpr (kPiece == 16)
           asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src + k * kElems) : "memory");
@@ -89,8 +109,8 @@ struct Stage {
       }
     }
   }
-  // Back into registers: the run's elements, as loaded.
-  __device__ __forceinline__ void read(Raw<T, RUN>& r) const {
+  // Back into registers, as loaded.
+  __device__ __forceinline__ void read(Got& r, const T*, int64_t) const {
 #pragma unroll
     for (int k = 0; k < kPieces; ++k) {
       Raw<T, kElems> q;
@@ -100,10 +120,52 @@ struct Stage {
     }
   }
 };
+
+// Single elements, each as the aligned 32-bit word that holds it (an asynchronous copy takes 4 bytes or
+// more).  The word's other half is a neighbour in memory: where there may be none (not `inner`: the
+// array's first and last token) the element is loaded by itself.
+template <typename T, typename S>
+struct Stage<T, S, false> {
+  static constexpr int RUN = S::kRun, kStep = Place<S, false>::kStep;
+  using Got = Raw<float, RUN>;
+  uint32_t word[RUN][kThreads];
+
+  __device__ __forceinline__ static bool upper(const T* q) {
+    return sizeof(T) == 2 && (reinterpret_cast<uintptr_t>(q) & 2) != 0;
+  }
+  __device__ __forceinline__ void fetch(const T* src, int64_t ld, int left, int nc, bool inner) {
+#pragma unroll
+    for (int i = 0; i < RUN; ++i) {
+      uint32_t* dst = &word[i][threadIdx.x];
+      const T* q = src + (size_t)(i * kStep) * ld;
+      if (i * kStep >= left || nc <= 0) {
+        *dst = 0u;
+      } else if (sizeof(T) == 4 || inner) {
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)),
+                     "l"(reinterpret_cast<uintptr_t>(q) & ~(uintptr_t)3)
+                     : "memory");
+      } else {
+        Raw<T, 1> r;
+        r.load(q);
+        *dst = upper(q) ? r.w[0] << 16 : r.w[0];
+      }
+    }
+  }
+  __device__ __forceinline__ void read(Got& r, const T* src, int64_t ld) const {
+#pragma unroll
+    for (int i = 0; i < RUN; ++i) {
+      const uint32_t w = word[i][threadIdx.x];
+      if constexpr (sizeof(T) == 4)
+        r.w[i] = w;
+      else
+        r.w[i] = upper(src + (size_t)(i * kStep) * ld) ? w & 0xFFFF0000u : w << 16;
+    }
+  }
+};
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
 
-template <typename T, int N>
+template <typename T, int N, bool VEC>
 struct __align__(16) Smem {
   using S = Shape<N>;
   float4 dxg[kTile][S::kCh];              // (Δ, Δ x, g, x), then (gx, gdt, gz, -); columns permuted
@@ -113,9 +175,9 @@ struct __align__(16) Smem {
   float2 sg[kTile][S::kCh];               // (σ(dt + bias), gy silu'(z)), columns permuted
   // states before tokens 0, 4, 8, 12, each thread's own; then, where it leaves room for three CTAs an
   // SM, the next tile's checkpoint (else that waits for the first of these to be free)
-  static constexpr bool kEarly = sizeof(T) == 2;
+  static constexpr bool kEarly = sizeof(T) == 2 && VEC;
   float4 snap[kTile / kSub + (kEarly ? 1 : 0)][2][kThreads];
-  Stage<T, S::kRun> x, dt, z, gy;
+  Stage<T, S, VEC> x, dt, z, gy;
 };
 
 // v[i ^ p] of 4 states held as two pairs, p the lane's order.
@@ -130,12 +192,13 @@ __device__ __forceinline__ void xor_order(float2 (&v)[2], int p) {
   }
 }
 
-template <typename T, int N>
+template <typename T, int N, bool VEC>
 __global__ void __launch_bounds__(kThreads, 3) scan_bwd_kernel(const __grid_constant__ ScanBwdParams p) {
   using S = Shape<N>;
-  constexpr int L = S::kLanes, CP = S::kPairs, CH = S::kCh, RUN = S::kRun, TT = S::kTokThreads;
+  constexpr int L = S::kLanes, CP = S::kPairs, CH = S::kCh, RUN = S::kRun;
   extern __shared__ __align__(16) unsigned char raw[];
-  Smem<T, N>& sm = *reinterpret_cast<Smem<T, N>*>(raw);
+  using SM = Smem<T, N, VEC>;
+  SM& sm = *reinterpret_cast<SM*>(raw);
   const ScanParams& f = p.f;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int ct = (int)(blockIdx.x % (unsigned)f.ctiles);
@@ -187,9 +250,9 @@ __global__ void __launch_bounds__(kThreads, 3) scan_bwd_kernel(const __grid_cons
 
   const float dsk = f.d != nullptr && cact[0] ? f.d[ct * CH + ch[0]] : 0.f;
 
-  // the loads' view: one token of the tile, a run of channels
-  const int lt = tid / TT, lq = tid % TT;
-  const int c0 = ct * CH + lq * RUN, nc = max(0, min(RUN, f.C - c0));
+  // the loads' view
+  const Place<S, VEC> at;
+  const int c0 = ct * CH + at.ch, nc = max(0, min(RUN, f.C - c0));
   float gd = 0.f, gbias = 0.f;  // of channel ch[0], over the tokens whose sums this lane ends up with
 
   for (int i = tid; i < CH; i += kThreads)
@@ -198,13 +261,16 @@ __global__ void __launch_bounds__(kThreads, 3) scan_bwd_kernel(const __grid_cons
 
   constexpr int QT = (S::kQuads + kThreads - 1) / kThreads;
   Raw<T, 4> bc[QT];
+  const auto src = [&](const void* a, int64_t ld, int ts) {  // this thread's first element of a tile
+    return static_cast<const T*>(a) + ((size_t)bb * f.T + (ts + at.t)) * ld + c0;
+  };
   const auto fetch = [&](int ts) {  // a tile's inputs, on their way
-    const int n = ts + lt < t1 ? nc : 0;  // n = 0: zeros, nothing read
-    const size_t row = (size_t)bb * f.T + (ts + lt);
-    sm.x.fetch(static_cast<const T*>(f.x) + row * f.ldx + c0, n, f.vec);
-    sm.dt.fetch(static_cast<const T*>(f.dt) + row * f.lddt + c0, n, f.vec);
-    sm.gy.fetch(static_cast<const T*>(p.gy) + row * f.C + c0, n, f.vec);
-    if (f.z != nullptr) sm.z.fetch(static_cast<const T*>(f.z) + row * f.ldz + c0, n, f.vec);
+    const int left = t1 - ts - at.t;  // none left: zeros, nothing read
+    const bool inner = (bb > 0 || ts > 0) && (bb < f.B - 1 || ts + kTile < f.T);
+    sm.x.fetch(src(f.x, f.ldx, ts), f.ldx, left, nc, inner);
+    sm.dt.fetch(src(f.dt, f.lddt, ts), f.lddt, left, nc, inner);
+    sm.gy.fetch(src(p.gy, f.C, ts), f.C, left, nc, inner);
+    if (f.z != nullptr) sm.z.fetch(src(f.z, f.ldz, ts), f.ldz, left, nc, inner);
     cp_async_commit();
 #pragma unroll
     for (int k = 0; k < QT; ++k) {
@@ -217,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 3) scan_bwd_kernel(const __grid_cons
       bc[k].load(static_cast<const T*>(is_c ? f.c : f.b) + rq * (is_c ? f.ldc : f.ldb) + s0, on ? 4 : 0, f.vec_bc);
     }
   };
-  constexpr bool kEarly = Smem<T, N>::kEarly;
+  constexpr bool kEarly = SM::kEarly;
   constexpr int kCk = kEarly ? kTile / kSub : 0;
   const auto fetch_state = [&](int ts) {  // the states before token ts
 #pragma unroll
@@ -237,20 +303,20 @@ __global__ void __launch_bounds__(kThreads, 3) scan_bwd_kernel(const __grid_cons
   fetch_state(ts);
 
   for (; ts >= t0; ts -= kTile) {
-    const bool tact = ts + lt < t1;
+    const auto on = [&](int i) { return ts + at.tok(i) < t1 && (VEC ? i : 0) < nc; };
     cp_async_wait_all();
     {
-      Raw<T, RUN> rx, rdt, rg, rz;
-      sm.x.read(rx);
-      sm.dt.read(rdt);
-      sm.gy.read(rg);
-      if (f.z != nullptr) sm.z.read(rz);
+      typename decltype(sm.x)::Got rx, rdt, rg, rz;
+      sm.x.read(rx, src(f.x, f.ldx, ts), f.ldx);
+      sm.dt.read(rdt, src(f.dt, f.lddt, ts), f.lddt);
+      sm.gy.read(rg, src(p.gy, f.C, ts), f.C);
+      if (f.z != nullptr) sm.z.read(rz, src(f.z, f.ldz, ts), f.ldz);
 #pragma unroll
       for (int i = 0; i < RUN; i += 2) {
-        const int cc = lq * RUN + i;
+        const int k0 = at.tok(i), k1 = at.tok(i + 1), w0 = S::col(at.chan(i)), w1 = S::col(at.chan(i + 1));
         float2 g = rg.pair(i / 2), e;
         const float2 x = rx.pair(i / 2);
-        const float2 v = add2(rdt.pair(i / 2), *reinterpret_cast<const float2*>(&sm.bias[cc]));
+        const float2 v = add2(rdt.pair(i / 2), make_float2(sm.bias[at.chan(i)], sm.bias[at.chan(i + 1)]));
         float2 dl = softplus2(v, e);
         const float2 d1 = add2(e, dup2(1.f)), r1 = make_float2(rcp_approx(d1.x), rcp_approx(d1.y)), er = mul2(e, r1);
         const float2 sig = make_float2(v.x >= 0.f ? r1.x : er.x, v.y >= 0.f ? r1.y : er.y);
@@ -261,13 +327,13 @@ __global__ void __launch_bounds__(kThreads, 3) scan_bwd_kernel(const __grid_cons
           g = mul2(g, zs);
         }
         // behind the end and past the last channel x = gy = 0 were fetched; Δ = 0 keeps the state
-        if (!tact || i >= nc) dl.x = 0.f;
-        if (!tact || i + 1 >= nc) dl.y = 0.f;
+        if (!on(i)) dl.x = 0.f;
+        if (!on(i + 1)) dl.y = 0.f;
         const float2 dx = mul2(dl, x);
-        sm.dxg[lt][S::col(cc)] = make_float4(dl.x, dx.x, g.x, x.x);
-        sm.dxg[lt][S::col(cc + 1)] = make_float4(dl.y, dx.y, g.y, x.y);
-        sm.sg[lt][S::col(cc)] = make_float2(sig.x, gpre.x);
-        sm.sg[lt][S::col(cc + 1)] = make_float2(sig.y, gpre.y);
+        sm.dxg[k0][w0] = make_float4(dl.x, dx.x, g.x, x.x);
+        sm.dxg[k1][w1] = make_float4(dl.y, dx.y, g.y, x.y);
+        sm.sg[k0][w0] = make_float2(sig.x, gpre.x);
+        sm.sg[k1][w1] = make_float2(sig.y, gpre.y);
       }
     }
 #pragma unroll
@@ -421,17 +487,29 @@ __global__ void __launch_bounds__(kThreads, 3) scan_bwd_kernel(const __grid_cons
     if (!kEarly && ts > t0) fetch_state(ts - kTile);
     __syncthreads();
 
-    if (tact && nc > 0) {
-      float ox[RUN], odt[RUN], oz[RUN];
+    if (ts + at.t < t1 && nc > 0) {
+      const size_t off = ((size_t)bb * f.T + ts + at.t) * f.C + c0;
+      if constexpr (VEC) {
+        float ox[RUN], odt[RUN], oz[RUN];
 #pragma unroll
-      for (int i = 0; i < RUN; ++i) {
-        const float4 d = sm.dxg[lt][S::col(lq * RUN + i)];
-        ox[i] = d.x, odt[i] = d.y, oz[i] = d.z;
+        for (int i = 0; i < RUN; ++i) {
+          const float4 d = sm.dxg[at.t][S::col(at.ch + i)];
+          ox[i] = d.x, odt[i] = d.y, oz[i] = d.z;
+        }
+        store_part<T, RUN>(static_cast<T*>(p.gx) + off, nc, true, ox);
+        store_part<T, RUN>(static_cast<T*>(p.gdt) + off, nc, true, odt);
+        if (p.gz != nullptr) store_part<T, RUN>(static_cast<T*>(p.gz) + off, nc, true, oz);
+      } else {
+#pragma unroll
+        for (int i = 0; i < RUN; ++i) {
+          if (!on(i)) continue;
+          const float4 d = sm.dxg[at.tok(i)][S::col(at.ch)];
+          const size_t o = off + (size_t)(i * Place<S, VEC>::kStep) * f.C;
+          static_cast<T*>(p.gx)[o] = IO<T>::from_f(d.x);
+          static_cast<T*>(p.gdt)[o] = IO<T>::from_f(d.y);
+          if (p.gz != nullptr) static_cast<T*>(p.gz)[o] = IO<T>::from_f(d.z);
+        }
       }
-      const size_t off = ((size_t)bb * f.T + ts + lt) * f.C + c0;
-      store_part<T, RUN>(static_cast<T*>(p.gx) + off, nc, f.vec, ox);
-      store_part<T, RUN>(static_cast<T*>(p.gdt) + off, nc, f.vec, odt);
-      if (p.gz != nullptr) store_part<T, RUN>(static_cast<T*>(p.gz) + off, nc, f.vec, oz);
     }
     float* part = p.part_bc + (((size_t)ct * f.B + bb) * f.T + ts) * (2 * N);
 #pragma unroll
@@ -443,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, 3) scan_bwd_kernel(const __grid_cons
       if (ts + tk < t1) part[i] = s;
     }
     // no barrier: the next tile's stores before its own barrier go only where this thread alone
-    // still reads (its run's columns of dxg, its stages) or nobody does (bc)
+    // still reads (its elements of dxg, its stages) or nobody does (bc)
   }
 
   const size_t prow = (size_t)bb * f.nseg + seg;
@@ -510,13 +588,21 @@ __global__ void __launch_bounds__(256) scan_bwd_param_kernel(int nparts, int C, 
   }
 }
 
+template <typename T, int N, bool VEC>
+cudaError_t launch_main(const ScanBwdParams& p, cudaStream_t st) {
+  static unsigned mask = 0;
+  constexpr int kSmem = (int)sizeof(Smem<T, N, VEC>);
+  const auto kernel = scan_bwd_kernel<T, N, VEC>;
+  const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kernel), kSmem, &mask);
+  if (e != cudaSuccess) return e;
+  kernel<<<(unsigned)p.f.ctiles * (unsigned)p.f.B * (unsigned)p.f.nseg, kThreads, kSmem, st>>>(p);
+  return cudaGetLastError();
+}
+
 template <typename T, int N>
 cudaError_t bwd_n(ScanBwdParams p, cudaStream_t st) {
-  static unsigned mask = 0;
   p.f.ctiles = (p.f.C + Shape<N>::kCh - 1) / Shape<N>::kCh;
-  constexpr int kSmem = (int)sizeof(Smem<T, N>);
-  cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(scan_bwd_kernel<T, N>), kSmem, &mask);
-  if (e != cudaSuccess) return e;
+  cudaError_t e;
   if (p.f.nseg > 1) {
     ScanParams r = p.f;
     r.x = p.gy;
@@ -529,8 +615,7 @@ cudaError_t bwd_n(ScanBwdParams p, cudaStream_t st) {
     r.seg_h0 = p.seg_g0;
     if ((e = launch_scan_reverse(sizeof(T) == 2, r, st)) != cudaSuccess) return e;
   }
-  scan_bwd_kernel<T, N><<<(unsigned)p.f.ctiles * (unsigned)p.f.B * (unsigned)p.f.nseg, kThreads, kSmem, st>>>(p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if ((e = p.f.vec ? launch_main<T, N, true>(p, st) : launch_main<T, N, false>(p, st)) != cudaSuccess) return e;
   const size_t n = (size_t)p.f.B * p.f.T * 2 * N;
   scan_bwd_bc_kernel<T><<<(unsigned)((n + 255) / 256), 256, 0, st>>>(p.f.ctiles, n, N, p.part_bc,
                                                                      static_cast<T*>(p.gb), static_cast<T*>(p.gc));

@@ -14,8 +14,9 @@
 //
 // Mapping.  A thread owns 4 states of one channel, the lanes of a warp are channels; a CTA owns 16
 // or 32 channels of one batch row over one time segment, 32 tokens at a time:
-//   1. the inputs of a tile are read in runs of channels per thread (16 bytes in bf16 with N = 16),
-//      a tile ahead, left as loaded in registers until the tile is due; Δ and Δx go to shared
+//   1. the inputs of a tile are read in runs of channels per thread (16 bytes in bf16 with N = 16; off
+//      the 16-byte grid one by one, side by side in a warp: 4x1024x2561 bf16 0.126 ms, 0.151 with runs of
+//      single accesses, 0.096 for 2560 channels), a tile ahead, left as loaded in registers until the tile is due; Δ and Δx go to shared
 //      memory, so softplus is done once per element and not once per group of states, and B, C as
 //      fp32 rows;
 //   2. each thread walks the 32 tokens, reading 4 of them ahead; Σ_n over its 4 states goes to
@@ -57,7 +58,7 @@ struct Shape {
   static constexpr int kThreads = kCh * kGroups;
   static constexpr int kTile = 32;                          // tokens per tile
   static constexpr int kTokThreads = kThreads / kTile;      // threads per token in the tile's loads
-  static constexpr int kRun = kCh / kTokThreads;            // channels per thread there
+  static constexpr int kRun = kCh / kTokThreads;            // elements per thread there
   static constexpr int kQuads = kTile * N / 4 / kThreads;   // groups of 4 states of B (and C) per thread there
   static_assert(kTokThreads * kRun == kCh && kQuads * kThreads * 4 == kTile * N, "a tile's loads cover it");
   static_assert(kRun % 2 == 0, "channels are worked on in pairs");
@@ -79,24 +80,57 @@ struct __align__(16) Smem {
   float y[S::kGroups][S::kTile * S::kCh + (S::kCh & 31)];   // Σ C h over each group of 4 states
 };
 
+// A thread's elements of a tile.  VEC: a run of channels of one token, in wide accesses.  Else rows or
+// bases are off the 16-byte grid: one channel of every kGroups-th token, so that a warp's single
+// accesses lie side by side.
+template <typename S, bool VEC>
+struct Place {
+  int t, ch;  // the first element's token in the tile and channel in the CTA
+  __device__ __forceinline__ Place() {
+    const int tid = threadIdx.x;
+    t = VEC ? tid / S::kTokThreads : tid / S::kCh;
+    ch = VEC ? tid % S::kTokThreads * S::kRun : tid % S::kCh;
+  }
+  __device__ __forceinline__ int tok(int i) const { return VEC ? t : t + i * S::kGroups; }
+  __device__ __forceinline__ int chan(int i) const { return VEC ? ch + i : ch; }
+};
+
+// Its elements of one array as loaded; those at or past token t1 or channel C are zero.
+template <typename T, typename S, bool VEC>
+struct Elems {
+  Raw<T, VEC ? S::kRun : 1> r[VEC ? 1 : S::kRun];
+  // src: the first element; left: tokens from there to the segment's end, nc: channels to the last
+  __device__ __forceinline__ void load(const T* src, int64_t ld, int left, int nc) {
+    if constexpr (VEC) {
+      r[0].load(src, left > 0 ? nc : 0, true);
+    } else {
+#pragma unroll
+      for (int i = 0; i < S::kRun; ++i) {
+        r[i].zero();
+        if (i * S::kGroups < left && nc > 0) r[i].load(src + (size_t)(i * S::kGroups) * ld);
+      }
+    }
+  }
+  __device__ __forceinline__ float operator[](int i) const { return VEC ? r[0][i] : r[VEC ? 0 : i][0]; }
+};
+
 // One tile's inputs in registers, as loaded.
-template <typename T, typename S>
+template <typename T, typename S, bool VEC>
 struct Tile {
-  Raw<T, S::kRun> x, dt, z;
+  Elems<T, S, VEC> x, dt, z;
   Raw<T, 4> b[S::kQuads], c[S::kQuads];
 };
 
-// The tile at token ts: this thread's token is t, its channels c0 .. c0 + nc - 1.
-template <typename T, int N, typename S, Pass PASS>
-__device__ __forceinline__ void load_tile(Tile<T, S>& R, const ScanParams& p, int bb, int ts, int t, int t1, int c0,
-                                          int nc) {
-  const bool ok = t < t1;
-  const size_t row = (size_t)bb * p.T + (ok ? t : 0);
-  const int n = ok ? nc : 0;
-  R.x.load(static_cast<const T*>(p.x) + row * p.ldx + c0, n, p.vec);
-  R.dt.load(static_cast<const T*>(p.dt) + row * p.lddt + c0, n, p.vec);
+// The tile at token ts: this thread's first element is token t of channel c0, nc channels to the last.
+template <typename T, int N, typename S, Pass PASS, bool VEC>
+__device__ __forceinline__ void load_tile(Tile<T, S, VEC>& R, const ScanParams& p, int bb, int ts, int t, int t1,
+                                          int c0, int nc) {
+  const int left = t1 - t;
+  const size_t row = (size_t)bb * p.T + (left > 0 ? t : 0);
+  R.x.load(static_cast<const T*>(p.x) + row * p.ldx + c0, p.ldx, left, nc);
+  R.dt.load(static_cast<const T*>(p.dt) + row * p.lddt + c0, p.lddt, left, nc);
   if constexpr (PASS != Pass::kSummary)
-    if (p.z != nullptr) R.z.load(static_cast<const T*>(p.z) + row * p.ldz + c0, n, p.vec);
+    if (p.z != nullptr) R.z.load(static_cast<const T*>(p.z) + row * p.ldz + c0, p.ldz, left, nc);
 #pragma unroll
   for (int k = 0; k < S::kQuads; ++k) {
     const int id = threadIdx.x + k * S::kThreads, tq = ts + id / (N / 4), s0 = id % (N / 4) * 4;
@@ -121,11 +155,11 @@ struct Quad {
   }
 };
 
-template <typename T, int N, int CH_, Pass PASS>
+template <typename T, int N, int CH_, Pass PASS, bool VEC>
 __global__ void __launch_bounds__(Shape<N, CH_>::kThreads) scan_fwd_kernel(const __grid_constant__ ScanParams p) {
   using S = Shape<N, CH_>;
   using SM = Smem<N, S>;
-  constexpr int CH = S::kCh, RUN = S::kRun, TT = S::kTokThreads, TL = S::kTile;
+  constexpr int CH = S::kCh, RUN = S::kRun, TL = S::kTile;
   constexpr bool OUT = PASS == Pass::kOutputs, REV = PASS == Pass::kReverse;
   extern __shared__ __align__(16) unsigned char raw[];
   SM& sm = *reinterpret_cast<SM*>(raw);
@@ -137,15 +171,16 @@ __global__ void __launch_bounds__(Shape<N, CH_>::kThreads) scan_fwd_kernel(const
   const int seg = (int)(rest % (unsigned)nseg) + (REV ? 1 : 0), bb = (int)(rest / (unsigned)nseg);
   const int t0 = seg * p.seg_len, t1 = min(p.T, t0 + p.seg_len);
 
-  // the loads' view: one token of the tile, a run of channels, a run of states
-  const int lt = tid / TT, lq = tid % TT;
-  const int c0 = ct * CH + lq * RUN, nc = max(0, min(RUN, p.C - c0));
-  Tile<T, S> R;
+  // the loads' view
+  const Place<S, VEC> at;
+  const int c0 = ct * CH + at.ch, nc = max(0, min(RUN, p.C - c0));
+  Tile<T, S, VEC> R;
   const int first = REV ? t0 + (t1 - t0 - 1) / TL * TL : t0;  // the first tile worked on
-  load_tile<T, N, S, PASS>(R, p, bb, first, first + lt, t1, c0, nc);
-  float bias[RUN], dsk[RUN];
+  load_tile<T, N, S, PASS, VEC>(R, p, bb, first, first + at.t, t1, c0, nc);
+  constexpr int NC = VEC ? RUN : 1;  // channels of a thread
+  float bias[NC], dsk[NC];
 #pragma unroll
-  for (int i = 0; i < RUN; ++i) {
+  for (int i = 0; i < NC; ++i) {
     bias[i] = p.dt_bias != nullptr && i < nc ? p.dt_bias[c0 + i] : 0.f;
     dsk[i] = OUT && p.d != nullptr && i < nc ? p.d[c0 + i] : 0.f;
   }
@@ -180,12 +215,12 @@ __global__ void __launch_bounds__(Shape<N, CH_>::kThreads) scan_fwd_kernel(const
   float sumdt = 0.f;
 
   for (int ts = first; ts >= t0 && ts < t1; ts += REV ? -TL : TL) {
-    const bool tact = ts + lt < t1;
+    const auto on = [&](int i) { return ts + at.tok(i) < t1 && (VEC ? i : 0) < nc; };
     float x[RUN], z[RUN];
 #pragma unroll
     for (int i = 0; i < RUN; i += 2) {
       float2 e;
-      const float2 dl = softplus2(make_float2(R.dt[i] + bias[i], R.dt[i + 1] + bias[i + 1]), e);
+      const float2 dl = softplus2(make_float2(R.dt[i] + bias[VEC ? i : 0], R.dt[i + 1] + bias[VEC ? i + 1 : 0]), e);
       x[i] = R.x[i], x[i + 1] = R.x[i + 1];
       if constexpr (OUT) z[i] = R.z[i], z[i + 1] = R.z[i + 1];
       float2 in = make_float2(dl.x * x[i], dl.y * x[i + 1]);
@@ -193,9 +228,13 @@ __global__ void __launch_bounds__(Shape<N, CH_>::kThreads) scan_fwd_kernel(const
         in = make_float2(x[i], x[i + 1]);
         if (p.z != nullptr) in = make_float2(x[i] * (R.z[i] * sigmoid_ex2(R.z[i])), x[i + 1] * (R.z[i + 1] * sigmoid_ex2(R.z[i + 1])));
       }
-      const bool on0 = tact && i < nc, on1 = tact && i + 1 < nc;
-      *reinterpret_cast<float4*>(&sm.dx[lt][lq * RUN + i]) =
-          make_float4(on0 ? dl.x : 0.f, on0 ? in.x : 0.f, on1 ? dl.y : 0.f, on1 ? in.y : 0.f);
+      const float2 u = on(i) ? make_float2(dl.x, in.x) : dup2(0.f), v = on(i + 1) ? make_float2(dl.y, in.y) : dup2(0.f);
+      if constexpr (VEC) {
+        *reinterpret_cast<float4*>(&sm.dx[at.t][at.ch + i]) = make_float4(u.x, u.y, v.x, v.y);
+      } else {
+        sm.dx[at.tok(i)][at.ch] = u;
+        sm.dx[at.tok(i + 1)][at.ch] = v;
+      }
     }
 #pragma unroll
     for (int k = 0; k < S::kQuads; ++k) {
@@ -204,7 +243,7 @@ __global__ void __launch_bounds__(Shape<N, CH_>::kThreads) scan_fwd_kernel(const
       if constexpr (OUT) *reinterpret_cast<float4*>(q.c) = make_float4(R.c[k][0], R.c[k][1], R.c[k][2], R.c[k][3]);
     }
     const int tn = REV ? ts - TL : ts + TL;
-    if (tn >= t0 && tn < t1) load_tile<T, N, S, PASS>(R, p, bb, tn, tn + lt, t1, c0, nc);
+    if (tn >= t0 && tn < t1) load_tile<T, N, S, PASS, VEC>(R, p, bb, tn, tn + at.t, t1, c0, nc);
     __syncthreads();
 
 #pragma unroll 1
@@ -244,14 +283,19 @@ __global__ void __launch_bounds__(Shape<N, CH_>::kThreads) scan_fwd_kernel(const
     __syncthreads();
 
     if constexpr (OUT) {
-      if (p.y != nullptr && tact && nc > 0) {
+      if (p.y != nullptr && nc > 0 && ts + at.t < t1) {
         float o[RUN];
 #pragma unroll
-        for (int i = 0; i < RUN; ++i) o[i] = dsk[i] * x[i];
+        for (int i = 0; i < RUN; ++i) o[i] = dsk[VEC ? i : 0] * x[i];
 #pragma unroll
         for (int g = 0; g < S::kGroups; ++g) {
           float v[RUN];
-          load_vec<float, RUN>(&sm.y[g][lt * CH + lq * RUN], v);
+          if constexpr (VEC) {
+            load_vec<float, RUN>(&sm.y[g][at.t * CH + at.ch], v);
+          } else {
+#pragma unroll
+            for (int i = 0; i < RUN; ++i) v[i] = sm.y[g][at.tok(i) * CH + at.ch];
+          }
 #pragma unroll
           for (int i = 0; i < RUN; ++i) o[i] += v[i];
         }
@@ -259,7 +303,14 @@ __global__ void __launch_bounds__(Shape<N, CH_>::kThreads) scan_fwd_kernel(const
 #pragma unroll
           for (int i = 0; i < RUN; ++i) o[i] *= z[i] * sigmoid_ex2(z[i]);
         }
-        store_part<T, RUN>(static_cast<T*>(p.y) + ((size_t)bb * p.T + ts + lt) * p.C + c0, nc, p.vec, o);
+        T* y = static_cast<T*>(p.y) + ((size_t)bb * p.T + ts + at.t) * p.C + c0;
+        if constexpr (VEC) {
+          store_part<T, RUN>(y, nc, true, o);
+        } else {
+#pragma unroll
+          for (int i = 0; i < RUN; ++i)
+            if (on(i)) y[(size_t)(i * S::kGroups) * p.C] = IO<T>::from_f(o[i]);
+        }
       }
     }
   }
@@ -274,16 +325,21 @@ __global__ void __launch_bounds__(Shape<N, CH_>::kThreads) scan_fwd_kernel(const
   }
 }
 
-template <typename T, int N, int CH, Pass PASS>
-cudaError_t launch_pass(const ScanParams& p, cudaStream_t st) {
+template <typename T, int N, int CH, Pass PASS, bool VEC>
+cudaError_t launch_as(const ScanParams& p, cudaStream_t st) {
   constexpr int kThreads = Shape<N, CH>::kThreads, kSmem = (int)sizeof(Smem<N, Shape<N, CH>>);
   static unsigned mask = 0;
-  const auto kernel = scan_fwd_kernel<T, N, CH, PASS>;
+  const auto kernel = scan_fwd_kernel<T, N, CH, PASS, VEC>;
   const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kernel), kSmem, &mask);
   if (e != cudaSuccess) return e;
   const unsigned segs = (unsigned)(PASS == Pass::kOutputs ? p.nseg : p.nseg - 1);
   kernel<<<(unsigned)p.ctiles * (unsigned)p.B * segs, kThreads, kSmem, st>>>(p);
   return cudaGetLastError();
+}
+
+template <typename T, int N, int CH, Pass PASS>
+cudaError_t launch_pass(const ScanParams& p, cudaStream_t st) {
+  return p.vec ? launch_as<T, N, CH, PASS, true>(p, st) : launch_as<T, N, CH, PASS, false>(p, st);
 }
 
 template <typename T, int N>

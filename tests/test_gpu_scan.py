@@ -93,6 +93,24 @@ def test_b_and_c_off_the_16_byte_grid(cuda_device, at):
     ref.check_all(_backward(q, ck), r)
 
 
+@DT
+@pytest.mark.parametrize("shape", [(2, 300, 97, 16), (1, 517, 131, 8), (2, 90, 35, 32), (1, 70, 21, 64)], ids=str)
+def test_rows_that_start_anywhere(cuda_device, shape, dtype):
+    # every array a part of rows of an odd length at an odd place, over several tiles and segments: single
+    # accesses, in bf16 as halves of 32-bit words; NaN around the parts stays there
+    p, v = ref.scan_inputs(*shape, seed=38, dtype=dtype)
+    r = ref.scan(**_cpu(p, v))
+    q = _dev(p, v, cuda_device)
+    B, T, C, _ = shape
+    for n, (k, at) in enumerate((("x", 1), ("dt", 2), ("z", 3))):
+        rows = torch.full((B, T, C + 4 + n % 2), float("nan"), dtype=dtype, device=cuda_device)
+        rows[..., at: at + C] = q[k]
+        q[k] = rows[..., at: at + C]
+    y, h, ck = _forward(q, return_state=True, checkpoints=True)
+    ref.check_all(dict(y=y, h=h), r)
+    ref.check_all(_backward(q, ck), r)
+
+
 def test_step_of_many_streams(cuda_device):
     # more streams than the grid's second dimension holds; rows of every part against single-stream calls
     B, C, N = 70001, 4, 8
