@@ -24,7 +24,7 @@ bool aligned(size_t bytes, std::initializer_list<const void*> ptrs) {
   return true;
 }
 
-// Every length a multiple of a 16-byte access's elements.
+// Every length a multiple of an access's elements.
 bool vec_len(int vec, std::initializer_list<int64_t> lens) {
   for (int64_t l : lens)
     if (l % vec != 0) return false;
@@ -41,6 +41,13 @@ bool grid_ok(double blocks) { return blocks <= (double)INT_MAX; }
 extern "C" {
 
 // ------------------------------------------------------------------ causal convolution
+static int conv_width(int64_t C, int64_t ldx, size_t esz, const float* weight,
+                      std::initializer_list<const void*> acts) {
+  for (int v = 4; v >= 2; v /= 2)
+    if (aligned(v * esz, acts) && aligned(16, {weight}) && vec_len(v, {C, ldx})) return v;
+  return 1;
+}
+
 size_t rwkv_causal_conv_backward_workspace_bytes(int64_t B, int64_t T, int64_t C, int64_t W) {
   if (B <= 0 || T <= 0 || C <= 0 || W < 2 || W > 4 || !fits_int(B) || !fits_int(T) || !fits_int(C)) return 0;
   if (!grid_ok((double)B * ((double)T / 64 + 1))) return 0;  // the call refuses it
@@ -82,8 +89,8 @@ rwkv_status rwkv_causal_conv_forward(int64_t B, int64_t T, int64_t C, int64_t W,
   p.y = y;
   p.state_in = state_in;
   p.state_out = state_out;
-  const bool vec = aligned(16, {weight, x, y, state_in, state_out}) && vec_len(16 / (int)esz, {C, ldx});
-  return launch_conv(ConvPass::kForward, bf16, vec, p, st) == cudaSuccess ? RWKV_OK : RWKV_ERR_CUDA;
+  const int width = conv_width(C, ldx, esz, weight, {x, y, state_in, state_out});
+  return launch_conv(ConvPass::kForward, bf16, width, p, st) == cudaSuccess ? RWKV_OK : RWKV_ERR_CUDA;
 }
 
 rwkv_status rwkv_causal_conv_backward(int64_t B, int64_t T, int64_t C, int64_t W, rwkv_dtype dtype,
@@ -137,9 +144,8 @@ rwkv_status rwkv_causal_conv_backward(int64_t B, int64_t T, int64_t C, int64_t W
   p.gweight = gweight;
   p.gbias = gbias;
   p.part = static_cast<float*>(workspace);
-  const bool vec =
-      aligned(16, {weight, x, gy, gx, state_in, gstate_out, gstate_in}) && vec_len(16 / (int)esz, {C, ldx});
-  return launch_conv(ConvPass::kBackward, bf16, vec, p, st) == cudaSuccess ? RWKV_OK : RWKV_ERR_CUDA;
+  const int width = conv_width(C, ldx, esz, weight, {x, gy, gx, state_in, gstate_out, gstate_in});
+  return launch_conv(ConvPass::kBackward, bf16, width, p, st) == cudaSuccess ? RWKV_OK : RWKV_ERR_CUDA;
 }
 
 rwkv_status rwkv_causal_conv_step(int64_t B, int64_t C, int64_t W, rwkv_dtype dtype, const float* weight,
@@ -168,8 +174,8 @@ rwkv_status rwkv_causal_conv_step(int64_t B, int64_t C, int64_t W, rwkv_dtype dt
   p.y = y;
   p.state_in = state_in;
   p.state_out = state_out;
-  const bool vec = aligned(16, {weight, x, y, state_in, state_out}) && vec_len(16 / (int)esz, {C, ldx});
-  return launch_conv(ConvPass::kStep, bf16, vec, p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+  const int width = conv_width(C, ldx, esz, weight, {x, y, state_in, state_out});
+  return launch_conv(ConvPass::kStep, bf16, width, p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? RWKV_OK
              : RWKV_ERR_CUDA;
 }

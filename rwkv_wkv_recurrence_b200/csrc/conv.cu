@@ -34,53 +34,101 @@ constexpr int kStepStreams = 2;  // streams per thread, step
 constexpr int kAhead = 8;        // tokens fetched together, forward
 constexpr int kBwdAhead = 8;     // tokens fetched together, backward
 
-// Channels are worked on in pairs (packed arithmetic); with V = 1 a pair's second half is idle.
+// Channels are worked on in pairs (packed arithmetic).  V > 1: a thread owns V neighbouring channels, in
+// one access.  V = 1, where rows or bases do not allow that: a pair is a channel of the first half and
+// the one as far into the second, each in accesses that lie side by side in a warp (4x4096x2561 bf16: 47
+// us and 105 backward; with one channel a thread 51 and 121; in fp32, 2048 tokens, 34 and 68, 34 and 91).
 template <int V>
 constexpr int kPairs = (V + 1) / 2;
+template <int V>
+constexpr int kOwn = V == 1 ? 2 : V;  // channels of a thread
+
+// Threads for C channels.
+template <int V>
+__host__ __device__ __forceinline__ int channel_threads(int C) {
+  return V == 1 ? (C + 1) / 2 : C / V;
+}
+// V = 1: from a thread's first channel c to its second; 0 behind the last of an odd number, where the
+// thread then works on c twice.
+template <int V>
+__device__ __forceinline__ int second(const ConvParams& p, int c) {
+  const int half = (p.C + 1) / 2;
+  return V == 1 && c + half < p.C ? half : 0;
+}
+
+// A thread's channels of one token as loaded.
+template <typename T, int V>
+struct Elem {
+  Raw<T, V> r[V == 1 ? 2 : 1];
+  __device__ __forceinline__ void load(const T* p, int off) {
+    r[0].load(p);
+    if constexpr (V == 1) r[1].load(p + off);
+  }
+  __device__ __forceinline__ void zero() {
+    r[0].zero();
+    if constexpr (V == 1) r[1].zero();
+  }
+  __device__ __forceinline__ float2 pair(int i) const {
+    if constexpr (V == 1)
+      return make_float2(r[0][0], r[1][0]);
+    else
+      return r[0].pair(i);
+  }
+};
+template <typename T, int V>
+__device__ __forceinline__ void store_elem(T* p, int off, const float2 (&o)[kPairs<V>]) {
+  if constexpr (V == 1) {
+    p[0] = IO<T>::from_f(o[0].x);
+    p[off] = IO<T>::from_f(off != 0 ? o[0].y : o[0].x);
+  } else {
+    store_pairs_as<T, V>(p, o);
+  }
+}
 
 // Element of the concatenation (state, x): position k < W-1 is state row k, the rest token k-(W-1).
 template <typename T, int V, int W>
-__device__ __forceinline__ void load_pos(const ConvParams& p, int b, int k, int c, float2 (&f)[kPairs<V>]) {
+__device__ __forceinline__ void load_pos(const ConvParams& p, int b, int k, int c, int off, float2 (&f)[kPairs<V>]) {
   const int t = k - (W - 1);
-  Raw<T, V> r;
+  Elem<T, V> r;
   if (t >= 0)
-    r.load(static_cast<const T*>(p.x) + ((size_t)b * p.T + t) * p.ldx + c);
+    r.load(static_cast<const T*>(p.x) + ((size_t)b * p.T + t) * p.ldx + c, off);
   else if (p.state_in != nullptr)
-    r.load(static_cast<const T*>(p.state_in) + ((size_t)b * (W - 1) + k) * p.C + c);
+    r.load(static_cast<const T*>(p.state_in) + ((size_t)b * (W - 1) + k) * p.C + c, off);
   else
     r.zero();
 #pragma unroll
   for (int i = 0; i < kPairs<V>; ++i) f[i] = r.pair(i);
 }
 
-// The filters and biases of channels c .. c + V - 1 (W V consecutive floats: wide loads where the
-// tensors are aligned for them, which V > 1 implies).
+// The filters and biases of a thread's channels (V > 1: W V consecutive floats, aligned for wide loads).
 template <int V, int W>
-__device__ __forceinline__ void load_filter(const ConvParams& p, int c, float2 (&w)[W][kPairs<V>],
+__device__ __forceinline__ void load_filter(const ConvParams& p, int c, int off, float2 (&w)[W][kPairs<V>],
                                             float2 (&bias)[kPairs<V>]) {
-  constexpr int Q = (V * W) % 4 == 0 ? 4 : (V * W) % 2 == 0 && V > 1 ? 2 : 1;
-  float f[V * W];
-  const float* q = p.weight + (size_t)c * W;
+  if constexpr (V == 1) {
 #pragma unroll
-  for (int i = 0; i < V * W; i += Q) {
-    if constexpr (Q == 4 && V > 1) {
-      const float4 x = *reinterpret_cast<const float4*>(q + i);
-      f[i] = x.x, f[i + 1] = x.y, f[i + 2] = x.z, f[i + 3] = x.w;
-    } else if constexpr (Q == 2) {
-      const float2 x = *reinterpret_cast<const float2*>(q + i);
-      f[i] = x.x, f[i + 1] = x.y;
-    } else {
+    for (int j = 0; j < W; ++j)
+      w[j][0] = make_float2(p.weight[(size_t)c * W + j], p.weight[(size_t)(c + off) * W + j]);
+    bias[0] = p.bias != nullptr ? make_float2(p.bias[c], p.bias[c + off]) : dup2(0.f);
+  } else {
+    constexpr int Q = (V * W) % 4 == 0 ? 4 : 2;
+    float f[V * W];
+    const float* q = p.weight + (size_t)c * W;
 #pragma unroll
-      for (int e = 0; e < Q; ++e) f[i + e] = q[i + e];
+    for (int i = 0; i < V * W; i += Q) {
+      if constexpr (Q == 4) {
+        const float4 x = *reinterpret_cast<const float4*>(q + i);
+        f[i] = x.x, f[i + 1] = x.y, f[i + 2] = x.z, f[i + 3] = x.w;
+      } else {
+        const float2 x = *reinterpret_cast<const float2*>(q + i);
+        f[i] = x.x, f[i + 1] = x.y;
+      }
     }
-  }
 #pragma unroll
-  for (int i = 0; i < kPairs<V>; ++i) {
-    const bool two = 2 * i + 1 < V;
+    for (int i = 0; i < kPairs<V>; ++i) {
 #pragma unroll
-    for (int j = 0; j < W; ++j) w[j][i] = make_float2(f[2 * i * W + j], two ? f[two ? (2 * i + 1) * W + j : 0] : 0.f);
-    bias[i] = dup2(0.f);
-    if (p.bias != nullptr) bias[i] = make_float2(p.bias[c + 2 * i], two ? p.bias[c + (two ? 2 * i + 1 : 0)] : 0.f);
+      for (int j = 0; j < W; ++j) w[j][i] = make_float2(f[2 * i * W + j], f[(2 * i + 1) * W + j]);
+      bias[i] = p.bias != nullptr ? make_float2(p.bias[c + 2 * i], p.bias[c + 2 * i + 1]) : dup2(0.f);
+    }
   }
 }
 
@@ -96,26 +144,26 @@ __device__ __forceinline__ void slide(float2 (&win)[W][P]) {
 template <typename T, int V, int W, bool SILU>
 __global__ void __launch_bounds__(kThreads) conv_fwd_kernel(const __grid_constant__ ConvParams p) {
   constexpr int P = kPairs<V>;
-  const int ncv = p.C / V;
+  const int ncv = channel_threads<V>(p.C);
   const long long id = (long long)blockIdx.x * kThreads + threadIdx.x;
   const int cv = (int)(id % ncv);
   const long long rest = id / ncv;
   const int seg = (int)(rest % p.nseg);
   const long long b64 = rest / p.nseg;
   if (b64 >= p.B) return;
-  const int b = (int)b64, c = cv * V;
+  const int b = (int)b64, c = cv * V, off = second<V>(p, c);
   const int t0 = seg * p.stretch, t1 = min(p.T, t0 + p.stretch);
   const T* xr = static_cast<const T*>(p.x) + ((size_t)b * p.T + t0) * p.ldx + c;
   T* yr = static_cast<T*>(p.y) + ((size_t)b * p.T + t0) * p.C + c;
-  Raw<T, V> nx[kAhead];
+  Elem<T, V> nx[kAhead];
 #pragma unroll
   for (int a = 0; a < kAhead; ++a)
-    if (t0 + a < t1) nx[a].load(xr + (size_t)a * p.ldx);
+    if (t0 + a < t1) nx[a].load(xr + (size_t)a * p.ldx, off);
   float2 w[W][P], bias[P], win[W][P];  // win[j]: the token j - (W-1) steps from the current one
-  load_filter<V, W>(p, c, w, bias);
+  load_filter<V, W>(p, c, off, w, bias);
 #pragma unroll
-  for (int j = 0; j < W - 1; ++j) load_pos<T, V, W>(p, b, t0 + j, c, win[j + 1]);
-  const auto token = [&](const Raw<T, V>& x, T* y) {
+  for (int j = 0; j < W - 1; ++j) load_pos<T, V, W>(p, b, t0 + j, c, off, win[j + 1]);
+  const auto token = [&](const Elem<T, V>& x, T* y) {
     slide(win);
     float2 o[P];
 #pragma unroll
@@ -126,20 +174,20 @@ __global__ void __launch_bounds__(kThreads) conv_fwd_kernel(const __grid_constan
       for (int j = 0; j < W; ++j) acc = fma2(w[j][i], win[j][i], acc);
       o[i] = SILU ? mul2(acc, sigmoid2(acc)) : acc;
     }
-    store_pairs_as<T, V>(y, o);
+    store_elem<T, V>(y, off, o);
   };
   for (int t = t0; t < t1; t += kAhead) {
-    Raw<T, V> cur[kAhead];
+    Elem<T, V> cur[kAhead];
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) cur[a] = nx[a];
     xr += (size_t)kAhead * p.ldx;
     if (t + 2 * kAhead <= t1) {
 #pragma unroll
-      for (int a = 0; a < kAhead; ++a) nx[a].load(xr + (size_t)a * p.ldx);
+      for (int a = 0; a < kAhead; ++a) nx[a].load(xr + (size_t)a * p.ldx, off);
     } else {
 #pragma unroll
       for (int a = 0; a < kAhead; ++a)
-        if (t + kAhead + a < t1) nx[a].load(xr + (size_t)a * p.ldx);
+        if (t + kAhead + a < t1) nx[a].load(xr + (size_t)a * p.ldx, off);
     }
     if (t + kAhead <= t1) {
 #pragma unroll
@@ -156,10 +204,10 @@ __global__ void __launch_bounds__(kThreads) conv_fwd_kernel(const __grid_constan
   if (seg == 0 && p.state_out != nullptr) {
     float2 last[W - 1][P];
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) load_pos<T, V, W>(p, b, p.T + j, c, last[j]);
+    for (int j = 0; j < W - 1; ++j) load_pos<T, V, W>(p, b, p.T + j, c, off, last[j]);
 #pragma unroll
     for (int j = 0; j < W - 1; ++j)
-      store_pairs_as<T, V>(static_cast<T*>(p.state_out) + ((size_t)b * (W - 1) + j) * p.C + c, last[j]);
+      store_elem<T, V>(static_cast<T*>(p.state_out) + ((size_t)b * (W - 1) + j) * p.C + c, off, last[j]);
   }
 }
 
@@ -168,15 +216,16 @@ __global__ void __launch_bounds__(kThreads) conv_fwd_kernel(const __grid_constan
 template <typename T, int V, int W, bool SILU>
 __global__ void __launch_bounds__(32 * kBwdWarps) conv_bwd_kernel(const __grid_constant__ ConvParams p) {
   constexpr int P = kPairs<V>;
-  __shared__ float red[kBwdWarps][W + 1][32 * V];
+  constexpr int CW = 32 * kOwn<V>;  // channels of a warp; V = 1: the first half's, then the second's
+  __shared__ float red[kBwdWarps][W + 1][CW];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int ncg = (p.C / V + 31) / 32;                        // channel groups of 32 V
-  const int nsg = (p.nseg + kBwdWarps - 1) / kBwdWarps;       // groups of stretches
+  const int ncv = channel_threads<V>(p.C), ncg = (ncv + 31) / 32;  // groups of 32 threads' channels
+  const int nsg = (p.nseg + kBwdWarps - 1) / kBwdWarps;            // groups of stretches
   const int cg = (int)(blockIdx.x % (unsigned)ncg);
   const unsigned rest = blockIdx.x / (unsigned)ncg;
   const int b = (int)(rest / (unsigned)nsg), seg = (int)(rest % (unsigned)nsg) * kBwdWarps + warp;
-  const int c = (cg * 32 + lane) * V;
-  const bool act = c < p.C && seg < p.nseg;
+  const int c = (cg * 32 + lane) * V, off = second<V>(p, c);
+  const bool act = cg * 32 + lane < ncv && seg < p.nseg;
   float2 gw[W + 1][P];
 #pragma unroll
   for (int j = 0; j <= W; ++j)
@@ -189,34 +238,34 @@ __global__ void __launch_bounds__(32 * kBwdWarps) conv_bwd_kernel(const __grid_c
     const T* xr = static_cast<const T*>(p.x) + ((size_t)b * p.T + t0) * p.ldx + c;
     const T* gr = static_cast<const T*>(p.gy) + ((size_t)b * p.T + t0) * p.C + c;
     T* gxr = static_cast<T*>(p.gx) + ((size_t)b * p.T + t0) * p.C + c;  // of the token being fetched for
-    Raw<T, V> nx[kBwdAhead], ng[kBwdAhead];
+    Elem<T, V> nx[kBwdAhead], ng[kBwdAhead];
     const auto fetch = [&](int t) {  // tokens t .. t + kBwdAhead - 1, xr and gr pointing at the first
       if (t + kBwdAhead <= p.T) {
 #pragma unroll
         for (int a = 0; a < kBwdAhead; ++a) {
-          nx[a].load(xr + (size_t)a * p.ldx);
-          ng[a].load(gr + (size_t)a * p.C);
+          nx[a].load(xr + (size_t)a * p.ldx, off);
+          ng[a].load(gr + (size_t)a * p.C, off);
         }
       } else {
 #pragma unroll
         for (int a = 0; a < kBwdAhead; ++a)
           if (t + a < p.T) {
-            nx[a].load(xr + (size_t)a * p.ldx);
-            ng[a].load(gr + (size_t)a * p.C);
+            nx[a].load(xr + (size_t)a * p.ldx, off);
+            ng[a].load(gr + (size_t)a * p.C, off);
           }
       }
     };
     fetch(t0);
-    load_filter<V, W>(p, c, w, bias);
+    load_filter<V, W>(p, c, off, w, bias);
 #pragma unroll
     for (int j = 0; j < W; ++j)
 #pragma unroll
       for (int i = 0; i < P; ++i) gp[j][i] = dup2(0.f);
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) load_pos<T, V, W>(p, b, t0 + j, c, win[j + 1]);
+    for (int j = 0; j < W - 1; ++j) load_pos<T, V, W>(p, b, t0 + j, c, off, win[j + 1]);
 
     // g of one token; its part of the weight gradients when the stretch owns it
-    const auto grad = [&](const Raw<T, V>& x, const Raw<T, V>& gy, bool own) {
+    const auto grad = [&](const Elem<T, V>& x, const Elem<T, V>& gy, bool own) {
       slide(gp);
       slide(win);
 #pragma unroll
@@ -246,7 +295,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps) conv_bwd_kernel(const __grid_c
         for (int j = 0; j < W; ++j) e[i] = fma2(w[j][i], gp[W - 1 - j][i], e[i]);
     };
     for (int t = t0; t < tend; t += kBwdAhead) {
-      Raw<T, V> cx[kBwdAhead], cg_[kBwdAhead];
+      Elem<T, V> cx[kBwdAhead], cg_[kBwdAhead];
 #pragma unroll
       for (int a = 0; a < kBwdAhead; ++a) cx[a] = nx[a], cg_[a] = ng[a];
       xr += (size_t)kBwdAhead * p.ldx;
@@ -263,7 +312,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps) conv_bwd_kernel(const __grid_c
 #pragma unroll
           for (int i = 0; i < P; ++i) o[i] = dup2(0.f);
           back(o);
-          store_pairs_as<T, V>(gxr + (ptrdiff_t)(a - (W - 1)) * p.C, o);
+          store_elem<T, V>(gxr + (ptrdiff_t)(a - (W - 1)) * p.C, off, o);
         }
       } else {
 #pragma unroll
@@ -283,18 +332,18 @@ __global__ void __launch_bounds__(32 * kBwdWarps) conv_bwd_kernel(const __grid_c
           if (to >= t0 || (seg == 0 && p.gstate_in != nullptr)) {
             float2 o[P];
             const int k = to + W - 1 - p.T;  // its row of the final state, when >= 0
-            Raw<T, V> e;
+            Elem<T, V> e;
             if (k >= 0 && p.gstate_out != nullptr)
-              e.load(static_cast<const T*>(p.gstate_out) + ((size_t)b * (W - 1) + k) * p.C + c);
+              e.load(static_cast<const T*>(p.gstate_out) + ((size_t)b * (W - 1) + k) * p.C + c, off);
             else
               e.zero();
 #pragma unroll
             for (int i = 0; i < P; ++i) o[i] = e.pair(i);
             back(o);
             if (to >= 0)
-              store_pairs_as<T, V>(gxr + (ptrdiff_t)(a - (W - 1)) * p.C, o);
+              store_elem<T, V>(gxr + (ptrdiff_t)(a - (W - 1)) * p.C, off, o);
             else
-              store_pairs_as<T, V>(static_cast<T*>(p.gstate_in) + ((size_t)b * (W - 1) + to + W - 1) * p.C + c, o);
+              store_elem<T, V>(static_cast<T*>(p.gstate_in) + ((size_t)b * (W - 1) + to + W - 1) * p.C + c, off, o);
           }
         }
       }
@@ -304,12 +353,14 @@ __global__ void __launch_bounds__(32 * kBwdWarps) conv_bwd_kernel(const __grid_c
 #pragma unroll
   for (int j = 0; j <= W; ++j)
 #pragma unroll
-    for (int i = 0; i < V; ++i) red[warp][j][lane * V + i] = i & 1 ? gw[j][i / 2].y : gw[j][i / 2].x;
+    for (int i = 0; i < kOwn<V>; ++i)
+      red[warp][j][V == 1 ? i * 32 + lane : lane * V + i] = i & 1 ? gw[j][i / 2].y : gw[j][i / 2].x;
   __syncthreads();
   float* part = p.part + (size_t)rest * (W + 1) * p.C;
-  for (int i = threadIdx.x; i < (W + 1) * 32 * V; i += 32 * kBwdWarps) {
-    const int j = i / (32 * V), cc = i % (32 * V), col = cg * 32 * V + cc;
-    if (col >= p.C) continue;
+  for (int i = threadIdx.x; i < (W + 1) * CW; i += 32 * kBwdWarps) {
+    const int j = i / CW, cc = i % CW, at = cg * 32 + (cc & 31);
+    const int col = V == 1 ? at + (cc < 32 ? 0 : ncv) : cg * CW + cc;
+    if (col >= p.C || (V == 1 && at >= ncv)) continue;
     float s = 0.f;
 #pragma unroll
     for (int k = 0; k < kBwdWarps; ++k) s += red[k][j][cc];
@@ -354,23 +405,23 @@ __global__ void __launch_bounds__(256) conv_reduce_kernel(int nparts, int C, int
 template <typename T, int V, int W>
 __global__ void __launch_bounds__(kThreads) conv_step_kernel(const __grid_constant__ ConvParams p) {
   constexpr int P = kPairs<V>;
-  const int ncv = p.C / V;
+  const int ncv = channel_threads<V>(p.C);
   const long long id = (long long)blockIdx.x * kThreads + threadIdx.x;
   const long long b0 = id / ncv * kStepStreams;
   if (b0 >= p.B) return;
-  const int c = (int)(id % ncv) * V, nb = (int)min((long long)kStepStreams, p.B - b0);
+  const int c = (int)(id % ncv) * V, off = second<V>(p, c), nb = (int)min((long long)kStepStreams, p.B - b0);
   float2 win[kStepStreams][W][P], w[W][P], bias[P];
 #pragma unroll
   for (int k = 0; k < kStepStreams; ++k) {
     const int b = (int)b0 + (k < nb ? k : 0);
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) load_pos<T, V, W>(p, b, j, c, win[k][j]);
-    Raw<T, V> x;
-    x.load(static_cast<const T*>(p.x) + (size_t)b * p.ldx + c);
+    for (int j = 0; j < W - 1; ++j) load_pos<T, V, W>(p, b, j, c, off, win[k][j]);
+    Elem<T, V> x;
+    x.load(static_cast<const T*>(p.x) + (size_t)b * p.ldx + c, off);
 #pragma unroll
     for (int i = 0; i < P; ++i) win[k][W - 1][i] = x.pair(i);
   }
-  load_filter<V, W>(p, c, w, bias);
+  load_filter<V, W>(p, c, off, w, bias);
 #pragma unroll
   for (int k = 0; k < kStepStreams; ++k) {
     if (k >= nb) break;
@@ -383,10 +434,10 @@ __global__ void __launch_bounds__(kThreads) conv_step_kernel(const __grid_consta
       for (int j = 0; j < W; ++j) acc = fma2(w[j][i], win[k][j][i], acc);
       o[i] = p.silu ? mul2(acc, sigmoid2(acc)) : acc;
     }
-    store_pairs_as<T, V>(static_cast<T*>(p.y) + b * p.C + c, o);
+    store_elem<T, V>(static_cast<T*>(p.y) + b * p.C + c, off, o);
 #pragma unroll
     for (int j = 0; j < W - 1; ++j)
-      store_pairs_as<T, V>(static_cast<T*>(p.state_out) + (b * (W - 1) + j) * p.C + c, win[k][j + 1]);
+      store_elem<T, V>(static_cast<T*>(p.state_out) + (b * (W - 1) + j) * p.C + c, off, win[k][j + 1]);
   }
 }
 
@@ -398,10 +449,10 @@ __global__ void copy_bytes_kernel(size_t n, const unsigned char* src, unsigned c
 
 template <typename T, int V, int W>
 cudaError_t fwd_vw(ConvParams p, cudaStream_t st) {
-  const long long threads = (long long)p.B * ((p.T + kFwdStretch - 1) / kFwdStretch) * (p.C / V);
+  const long long threads = (long long)p.B * ((p.T + kFwdStretch - 1) / kFwdStretch) * channel_threads<V>(p.C);
   p.stretch = threads < 148 * kThreads ? kShortStretch : kFwdStretch;
   p.nseg = (p.T + p.stretch - 1) / p.stretch;
-  const long long n = (long long)p.B * p.nseg * (p.C / V);
+  const long long n = (long long)p.B * p.nseg * channel_threads<V>(p.C);
   const auto kernel = p.silu ? conv_fwd_kernel<T, V, W, true> : conv_fwd_kernel<T, V, W, false>;
   kernel<<<(unsigned)((n + kThreads - 1) / kThreads), kThreads, 0, st>>>(p);
   return cudaGetLastError();
@@ -411,7 +462,7 @@ template <typename T, int V, int W>
 cudaError_t bwd_vw(ConvParams p, cudaStream_t st) {
   p.nseg = (p.T + kBwdStretch - 1) / kBwdStretch;
   const int nparts = conv_bwd_parts(p.B, p.T);
-  const int ncg = (p.C / V + 31) / 32;
+  const int ncg = (channel_threads<V>(p.C) + 31) / 32;
   const auto kernel = p.silu ? conv_bwd_kernel<T, V, W, true> : conv_bwd_kernel<T, V, W, false>;
   kernel<<<(unsigned)nparts * (unsigned)ncg, 32 * kBwdWarps, 0, st>>>(p);
   cudaError_t e = cudaGetLastError();
@@ -423,7 +474,7 @@ cudaError_t bwd_vw(ConvParams p, cudaStream_t st) {
 
 template <typename T, int V, int W>
 cudaError_t step_vw(const ConvParams& p, cudaStream_t st) {
-  const long long n = ((long long)p.B + kStepStreams - 1) / kStepStreams * (p.C / V);
+  const long long n = ((long long)p.B + kStepStreams - 1) / kStepStreams * channel_threads<V>(p.C);
   conv_step_kernel<T, V, W><<<(unsigned)((n + kThreads - 1) / kThreads), kThreads, 0, st>>>(p);
   return cudaGetLastError();
 }
@@ -450,9 +501,11 @@ int conv_bwd_parts(int B, int T) {
   return B * ((nseg + kBwdWarps - 1) / kBwdWarps);
 }
 
-cudaError_t launch_conv(ConvPass pass, bool bf16, bool vec, const ConvParams& p, cudaStream_t st) {
-  if (bf16) return vec ? run_v<__nv_bfloat16, 4>(pass, p, st) : run_v<__nv_bfloat16, 1>(pass, p, st);
-  return vec ? run_v<float, 2>(pass, p, st) : run_v<float, 1>(pass, p, st);
+cudaError_t launch_conv(ConvPass pass, bool bf16, int width, const ConvParams& p, cudaStream_t st) {
+  if (!bf16) return width >= 2 ? run_v<float, 2>(pass, p, st) : run_v<float, 1>(pass, p, st);
+  return width >= 4   ? run_v<__nv_bfloat16, 4>(pass, p, st)
+         : width >= 2 ? run_v<__nv_bfloat16, 2>(pass, p, st)
+                      : run_v<__nv_bfloat16, 1>(pass, p, st);
 }
 
 cudaError_t launch_copy_bytes(size_t n, const void* src, void* dst, cudaStream_t st) {

@@ -231,8 +231,9 @@ struct ConvParams {
 };
 enum class ConvPass { kForward, kBackward, kStep };
 int conv_bwd_parts(int B, int T);
-// vec: C, ldx and every base allow 16-byte accesses.
-cudaError_t launch_conv(ConvPass pass, bool bf16, bool vec, const ConvParams& p, cudaStream_t st);
+// width: channels (4, 2 or 1) that C, ldx and every base allow in one access; with 2 or more the filters
+// allow 16-byte accesses.
+cudaError_t launch_conv(ConvPass pass, bool bf16, int width, const ConvParams& p, cudaStream_t st);
 // dst[i] = src[i], or 0 without src.
 cudaError_t launch_copy_bytes(size_t n, const void* src, void* dst, cudaStream_t st);
 

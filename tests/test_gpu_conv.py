@@ -151,3 +151,25 @@ def test_same_bits_twice(cuda_device):
     a = rw.rwkv_causal_conv_backward(p["x"], p["w"], p["gy"], p["bias"], silu=True)
     b = rw.rwkv_causal_conv_backward(p["x"], p["w"], p["gy"], p["bias"], silu=True)
     assert all(torch.equal(s, t) for s, t in zip(a, b))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("W", [2, 3, 4])
+@pytest.mark.parametrize("C,pad,at", [(66, 0, 0), (10, 4, 2), (2, 0, 0), (66, 3, 0), (65, 0, 0), (63, 2, 1), (1, 0, 0)])
+def test_two_channels_a_thread(cuda_device, C, pad, at, W, dtype):
+    # even channel counts that are no multiple of 4 (neighbours in one access), odd ones and odd rows (a
+    # channel of each half); forward, backward and step, states in and out, the step's in place
+    p = _inputs(2, 70, C, W, 16, dtype)
+    wide = torch.full((2, 70, C + pad), float("nan"), dtype=dtype)
+    wide[..., at: at + C] = p["x"]
+    xv = wide.to(cuda_device)[..., at: at + C]
+    q = {k: v.to(cuda_device) for k, v in p.items()}
+    r = ref.conv(p["x"], p["w"], p["bias"], p["state"], True, p["gy"], p["gstate"])
+    y, so = rw.rwkv_causal_conv_forward(xv, q["w"], q["bias"], q["state"], silu=True, return_state=True)
+    gx, gw, gb, gs = rw.rwkv_causal_conv_backward(xv, q["w"], q["gy"], q["bias"], q["state"], q["gstate"], silu=True,
+                                                  want_gstate_in=True)
+    ref.check_all(dict(y=y, state=so, gx=gx, gw=gw, gbias=gb, gstate_in=gs), r)
+    st = q["state"].clone()
+    for t in range(3):
+        yt = rw.rwkv_causal_conv_step(xv[:, t].contiguous(), q["w"], st, q["bias"], silu=True)
+        assert torch.equal(yt, y[:, t]), t
