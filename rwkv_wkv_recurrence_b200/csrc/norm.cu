@@ -592,13 +592,16 @@ int resident_ctas(const void* kernel, int threads, int* known) {
   return n * kSMs;
 }
 
-// Rows between two of equal shift (a power of two): rows of a team are a multiple of it apart.
+// Rows between two of equal shift (a power of two): rows of a team are a multiple of it apart, unless
+// there is a team for every row.
 int shift_period(int N, int V) {
   int q = V;
   while (q > 1 && N % 2 == 0) q /= 2, N /= 2;
   return q;
 }
-int whole_periods(int slices, int q) { return std::max(1, slices / q) * q; }
+int whole_periods(int slices, int q, long long M) {
+  return (int)std::min<long long>(M, (long long)std::max(1, slices / q) * q);
+}
 
 template <bool BWD, typename T, int V, int K, int TS, bool SHIFT>
 cudaError_t run_team(NormParams p, cudaStream_t st) {
@@ -610,7 +613,7 @@ cudaError_t run_team(NormParams p, cudaStream_t st) {
     static int known[2] = {0, 0};
     const int ctas = resident_ctas(reinterpret_cast<const void*>(kernel), kCtaThreads<TS>, &known[gate]);
     p.slices = slices_for(p.M, p.G, (long long)ctas * kTeams<TS>, 1);
-    if (SHIFT) p.slices = whole_periods(p.slices, shift_period(p.N, V));
+    if (SHIFT) p.slices = whole_periods(p.slices, shift_period(p.N, V), p.M);
   }
   const long long teams = (long long)p.slices * p.G;
   const unsigned grid = (unsigned)((teams + kTeams<TS> - 1) / kTeams<TS>);
@@ -675,7 +678,7 @@ BwdPlan bwd_plan(long long M, int G, int N, bool bf16, NormAccess access) {
   const int ts = team_shape(row_vectors(N, v, shift), v).ts;
   const int teams = ts == 0 || ts > 256 ? 1 : 256 / ts;  // a CTA's
   int slices = slices_for(M, G, kBwdThreads / (ts == 0 ? kMaxTeam : ts), 4);
-  if (shift && ts != 0) slices = whole_periods(slices, shift_period(N, v));
+  if (shift && ts != 0) slices = whole_periods(slices, shift_period(N, v), M);
   return {slices, G == 1 ? (slices + teams - 1) / teams : slices};
 }
 

@@ -16,9 +16,9 @@
 // or 32 channels of one batch row over one time segment, 32 tokens at a time:
 //   1. the inputs of a tile are read in runs of channels per thread (16 bytes in bf16 with N = 16; off
 //      the 16-byte grid one by one, side by side in a warp: 4x1024x2561 bf16 0.126 ms, 0.151 with runs of
-//      single accesses, 0.096 for 2560 channels), a tile ahead, left as loaded in registers until the tile is due; Δ and Δx go to shared
-//      memory, so softplus is done once per element and not once per group of states, and B, C as
-//      fp32 rows;
+//      single accesses, 0.096 for 2560 channels), a tile ahead, left as loaded in registers until the
+//      tile is due; Δ and Δx go to shared memory, so softplus is done once per element and not once per
+//      group of states, and B, C as fp32 rows;
 //   2. each thread walks the 32 tokens, reading 4 of them ahead; Σ_n over its 4 states goes to
 //      shared memory per group of states (folding a channel's states over lanes instead costs
 //      three shuffles and nine selects and adds per 4 tokens, and measured 0.473 ms; two channels
@@ -29,8 +29,8 @@
 // Few channels, long axis: time is cut into segments.  A first launch runs every segment but the
 // last from a zero state and keeps the state it reaches and ΣΔ; the state entering segment s is
 // then folded from these in order (the decay over a segment is exp(A ΣΔ)) by the CTA that needs
-// it, in the second launch, which writes the outputs (1x8192x2048: 0.37 ms whole, 0.21 in 9 segments).  Sums run in a fixed order: the same inputs
-// give the same bits.
+// it, in the second launch, which writes the outputs (1x8192x2048: 0.37 ms whole, 0.21 in 9 segments).
+// Sums run in a fixed order: the same inputs give the same bits.
 #include <algorithm>
 
 #include "launch.h"
@@ -226,7 +226,10 @@ __global__ void __launch_bounds__(Shape<N, CH_>::kThreads) scan_fwd_kernel(const
       float2 in = make_float2(dl.x * x[i], dl.y * x[i + 1]);
       if constexpr (REV) {
         in = make_float2(x[i], x[i + 1]);
-        if (p.z != nullptr) in = make_float2(x[i] * (R.z[i] * sigmoid_ex2(R.z[i])), x[i + 1] * (R.z[i + 1] * sigmoid_ex2(R.z[i + 1])));
+        if (p.z != nullptr) {
+          const float za = R.z[i], zb = R.z[i + 1];
+          in = make_float2(in.x * (za * sigmoid_ex2(za)), in.y * (zb * sigmoid_ex2(zb)));
+        }
       }
       const float2 u = on(i) ? make_float2(dl.x, in.x) : dup2(0.f), v = on(i + 1) ? make_float2(dl.y, in.y) : dup2(0.f);
       if constexpr (VEC) {
