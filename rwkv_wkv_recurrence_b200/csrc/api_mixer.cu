@@ -280,8 +280,8 @@ ScanBwdWs scan_bwd_ws(int64_t B, int64_t T, int64_t C, int64_t N, bool have_ckpt
 bool scan_grid_ok(int64_t B, int64_t T, int64_t C, int64_t N) {
   const double ch = (double)scan_fwd_channels((int)N);
   return grid_ok((double)B * ((double)C / ch + 1) * ((double)T / 32 + 1)) &&
-         grid_ok((double)B * (double)T * (double)(2 * N) / 256 + 1) &&
-         grid_ok(((double)C * (double)N + 2 * (double)C) / 256 + 1) && T <= INT_MAX - 64;
+         grid_ok(((double)B * (double)T * (double)(2 * N) + (double)C * (double)(N + 2)) / 256 + 2) &&
+         T <= INT_MAX - 64;
 }
 
 struct ScanIn {

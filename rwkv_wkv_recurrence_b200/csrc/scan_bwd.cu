@@ -545,46 +545,45 @@ __global__ void __launch_bounds__(kThreads, 3) scan_bwd_kernel(const __grid_cons
   }
 }
 
-// gb, gc: the channel tiles' parts added in order, rounded once.
-template <typename T>
-__global__ void __launch_bounds__(256) scan_bwd_bc_kernel(int ctiles, size_t n, int N, const float* __restrict__ part,
-                                                          T* gb, T* gc) {
-  const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;  // over [B,T][2][N]
-  if (i >= n) return;
-  float s = 0.f;
-  for (int k = 0; k < ctiles; ++k) s += part[(size_t)k * n + i];
-  const size_t row = i / (2 * N);
-  const int j = (int)(i % (2 * N));
-  (j < N ? gc : gb)[row * N + j % N] = IO<T>::from_f(s);
-}
-
 // n floats `stride` apart, added in order, 8 loads at a time.
-__device__ __forceinline__ double sum_parts(const float* __restrict__ p, int n, size_t stride) {
-  double s = 0.0;
+template <typename S>
+__device__ __forceinline__ S sum_parts(const float* __restrict__ p, int n, size_t stride) {
+  S s = 0;
   int k = 0;
   for (; k + 8 <= n; k += 8) {
     float v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = p[(size_t)(k + i) * stride];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s += (double)v[i];
+    for (int i = 0; i < 8; ++i) s += (S)v[i];
   }
-  for (; k < n; ++k) s += (double)p[(size_t)k * stride];
+  for (; k < n; ++k) s += (S)p[(size_t)k * stride];
   return s;
 }
 
-// ga_log [C,N], then gd [C] and gdt_bias [C]: the parts of the batch rows and segments in order.
-__global__ void __launch_bounds__(256) scan_bwd_param_kernel(int nparts, int C, int N, const float* __restrict__ a_log,
-                                                             const float* __restrict__ part_a,
-                                                             const float* __restrict__ part_v, float* ga_log, float* gd,
-                                                             float* gdt_bias) {
-  const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x, na = (size_t)C * N;
-  if (i < na) {
-    ga_log[i] = (float)(sum_parts(part_a + i, nparts, na) * -(double)expf(a_log[i]));
-  } else if (i < na + 2 * (size_t)C) {
-    const size_t j = i - na;
-    float* dst = j < (size_t)C ? gd : gdt_bias;
-    if (dst != nullptr) dst[j % C] = (float)sum_parts(part_v + j, nparts, 2 * (size_t)C);
+// What the parts add up to, in one launch.  The first `vblocks` blocks: ga_log [C,N], then gd [C] and
+// gdt_bias [C], the parts of the batch rows and segments in order.  The rest: gb, gc, the channel tiles'
+// parts in order, rounded once.
+template <typename T>
+__global__ void __launch_bounds__(256) scan_bwd_sum_kernel(const __grid_constant__ ScanBwdParams p, unsigned vblocks) {
+  const int N = p.f.N, C = p.f.C;
+  if (blockIdx.x >= vblocks) {
+    const size_t i = (size_t)(blockIdx.x - vblocks) * 256 + threadIdx.x, n = (size_t)p.f.B * p.f.T * 2 * N;
+    if (i >= n) return;  // over [B,T][2][N]
+    const float s = sum_parts<float>(p.part_bc + i, p.f.ctiles, n);
+    const size_t row = i / (2 * N);
+    const int j = (int)(i % (2 * N));
+    static_cast<T*>(j < N ? p.gc : p.gb)[row * N + j % N] = IO<T>::from_f(s);
+  } else {
+    const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x, na = (size_t)C * N;
+    const int nparts = p.f.B * p.f.nseg;
+    if (i < na) {
+      p.ga_log[i] = (float)(sum_parts<double>(p.part_a + i, nparts, na) * -(double)expf(p.f.a_log[i]));
+    } else if (i < na + 2 * (size_t)C) {
+      const size_t j = i - na;
+      float* dst = j < (size_t)C ? p.gd : p.gdt_bias;
+      if (dst != nullptr) dst[j % C] = (float)sum_parts<double>(p.part_v + j, nparts, 2 * (size_t)C);
+    }
   }
 }
 
@@ -616,13 +615,9 @@ cudaError_t bwd_n(ScanBwdParams p, cudaStream_t st) {
     if ((e = launch_scan_reverse(sizeof(T) == 2, r, st)) != cudaSuccess) return e;
   }
   if ((e = p.f.vec ? launch_main<T, N, true>(p, st) : launch_main<T, N, false>(p, st)) != cudaSuccess) return e;
-  const size_t n = (size_t)p.f.B * p.f.T * 2 * N;
-  scan_bwd_bc_kernel<T><<<(unsigned)((n + 255) / 256), 256, 0, st>>>(p.f.ctiles, n, N, p.part_bc,
-                                                                     static_cast<T*>(p.gb), static_cast<T*>(p.gc));
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  const size_t m = (size_t)p.f.C * N + 2 * (size_t)p.f.C;
-  scan_bwd_param_kernel<<<(unsigned)((m + 255) / 256), 256, 0, st>>>(p.f.B * p.f.nseg, p.f.C, N, p.f.a_log, p.part_a,
-                                                                    p.part_v, p.ga_log, p.gd, p.gdt_bias);
+  const size_t n = (size_t)p.f.B * p.f.T * 2 * N, m = (size_t)p.f.C * N + 2 * (size_t)p.f.C;
+  const unsigned vblocks = (unsigned)((m + 255) / 256);
+  scan_bwd_sum_kernel<T><<<vblocks + (unsigned)((n + 255) / 256), 256, 0, st>>>(p, vblocks);
   return cudaGetLastError();
 }
 
