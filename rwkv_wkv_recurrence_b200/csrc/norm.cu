@@ -15,9 +15,9 @@
 // difference of large sums.  A team keeps its group and strides over the rows, so w and b, and the
 // backward's column sums, stay in registers; teams of neighbouring groups are neighbours, so a
 // CTA's accesses are contiguous.  Column sums go to the workspace per team and are added in order
-// by a second kernel: no atomics, the same inputs give the same bits.  Groups wider than 1024 vectors
-// (2048 in fp32) take a kernel that reads the row again for each sum (from L1 / L2).  Rows are fetched a
-// turn ahead.  Gated heads 16384x40x64 bf16: 43.6 us forward (5.8 TB/s), 78 and 6 for the column sums
+// by a second kernel: no atomics, the same inputs give the same bits.  Groups wider than 2048 vectors
+// take a kernel that reads the row again for each sum (from L1 / L2).  Rows are fetched a turn ahead.
+// Gated heads 16384x40x64 bf16: 43.6 us forward (5.8 TB/s), 78 and 6 for the column sums
 // backward (5.4 TB/s); fp32 8192x768: 9.2, 13.6 and 4.8.
 //
 // Rows of any length.  Where rows do not start on 16-byte boundaries a team's vectors are laid on those
@@ -279,8 +279,12 @@ __global__ void __launch_bounds__(kCtaThreads<TS>) norm_fwd_kernel(const __grid_
 }
 
 template <typename T, int V, int K, int TS, bool GATE, bool SHIFT>
-__global__ void __launch_bounds__(kCtaThreads<TS>) norm_bwd_kernel(const __grid_constant__ NormParams p) {
+__global__ void __launch_bounds__(kCtaThreads<TS>, TS == 512 ? 1 : 0) norm_bwd_kernel(const __grid_constant__ NormParams p) {
   constexpr int P = (V + 1) / 2;
+  // Where a row's three inputs, parameters and sums pass what 128 registers a thread hold, parameters are read
+  // again for each row (from L1) and no row is fetched ahead: fewer spills (4096 x 6832 fp32 175 us, 219
+  // otherwise; x 12288 bf16 225, 577).  Off the 16-byte grid parameters come one by one, and it does not pay.
+  constexpr bool kLean = TS == 512 && K >= 3 && GATE && !SHIFT;
   __shared__ float2 buf[TeamSum<TS>::kBuf];
   TeamSum<TS> sum{buf};
   const Team<TS> tm(p);
@@ -306,19 +310,15 @@ __global__ void __launch_bounds__(kCtaThreads<TS>) norm_bwd_kernel(const __grid_
     rz.load(z_at, cols, inner);
   }
   float2 w[K][P], b[K][P], gw[K][P], gb[K][P];
-#pragma unroll
-  for (int k = 0; k < K; ++k) {
+  const auto params = [&](int k) {
     load_params<V>(p.weight + (size_t)tm.g * p.N, cols, k, w[k]);
     if constexpr (GATE) load_params<V>(p.bias != nullptr ? p.bias + (size_t)tm.g * p.N : nullptr, cols, k, b[k]);
+  };
+  if constexpr (!kLean) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) params(k);
   }
-#pragma unroll
-  for (int k = 0; k < K; ++k)
-#pragma unroll
-    for (int i = 0; i < P; ++i) gw[k][i] = gb[k][i] = dup2(0.f);
-  for (long long it = 0; it < tm.turns; ++it) {
-    const bool on = m < p.M;
-    RowPart<T, V, K, TS, SHIFT> cx = rx, cg = rg, cz = rz;
-    m += tm.step;
+  const auto fetch = [&] {  // row m
     if (m < p.M) {
       x_at += stride;
       g_at += stride;
@@ -329,6 +329,16 @@ __global__ void __launch_bounds__(kCtaThreads<TS>) norm_bwd_kernel(const __grid_
         rz.load(z_at, cols, m < last);
       }
     }
+  };
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+#pragma unroll
+    for (int i = 0; i < P; ++i) gw[k][i] = gb[k][i] = dup2(0.f);
+  for (long long it = 0; it < tm.turns; ++it) {
+    const bool on = m < p.M;
+    RowPart<T, V, K, TS, SHIFT> cx = rx, cg = rg, cz = rz;
+    m += tm.step;
+    if (!kLean) fetch();
     cx.mask(cols);
     cg.mask(cols);
     if constexpr (GATE) cz.mask(cols);
@@ -336,7 +346,8 @@ __global__ void __launch_bounds__(kCtaThreads<TS>) norm_bwd_kernel(const __grid_
     const float rstd = center<T, V, K, TS, SHIFT>(cx, x, cols, inv_n, p.eps, sum);
     float2 su = dup2(0.f), sx = dup2(0.f);
 #pragma unroll
-    for (int k = 0; k < K; ++k)
+    for (int k = 0; k < K; ++k) {
+      if constexpr (kLean) params(k);
 #pragma unroll
       for (int i = 0; i < P; ++i) {
         x[k][i] = mul2(x[k][i], dup2(rstd));
@@ -355,6 +366,7 @@ __global__ void __launch_bounds__(kCtaThreads<TS>) norm_bwd_kernel(const __grid_
         su = add2(su, u[k][i]);
         sx = fma2(u[k][i], x[k][i], sx);
       }
+    }
     const float2 r = sum(su.x + su.y, sx.x + sx.y);
     if (on) {
       const float2 c0 = dup2(-rstd * r.x * inv_n), c1 = dup2(-rstd * r.y * inv_n);
@@ -370,6 +382,7 @@ __global__ void __launch_bounds__(kCtaThreads<TS>) norm_bwd_kernel(const __grid_
     }
     gx_at += stride;
     if constexpr (GATE) gz_at += stride;
+    if (kLean) fetch();
   }
   // With one group a CTA's teams hold the same columns and add up in shared memory, in order; else
   // each writes its own.
@@ -548,16 +561,15 @@ __global__ void __launch_bounds__(1024) norm_reduce_kernel(int slices, int C, co
   }
 }
 
-// Threads of a team and vectors (of v elements) per thread for nv vectors a group; 0 threads: the wide
-// kernel.  Few threads with several vectors meet faster than many with one: 512 x 1 for 4096 columns in
+// Threads of a team and vectors per thread for nv vectors a group; 0 threads: the wide kernel.  Few threads with several vectors meet faster than many with one: 512 x 1 for 4096 columns in
 // bf16 took 72 us forward and 145 backward (16384 rows), 256 x 2 51 and 84; 128 x 3 for 2560 columns 9.6
-// and 22 (4096 rows), 256 x 2 12.7 and 25.  Three and four vectors of 512 threads hold their registers
-// in fp32 only, the gated backward not quite: 4096x6832 gated fp32 54 us and 222, with the wide kernel 177
-// and 553.
+// and 22 (4096 rows), 256 x 2 12.7 and 25.  Three and four vectors of 512 threads do not all stay in
+// registers, but beat the wide kernel: 4096x6832 gated fp32 54 us and 175, 177 and 553; 4096x16384 bf16
+// 62 and 193, 170 and 953.
 struct TeamShape {
   int ts, k;
 };
-TeamShape team_shape(int nv, int v) {
+TeamShape team_shape(int nv) {
   if (nv <= 8) return {8, 1};
   if (nv <= 16) return {16, 1};
   if (nv <= 32) return {32, 1};
@@ -569,8 +581,8 @@ TeamShape team_shape(int nv, int v) {
   if (nv <= 512) return {256, 2};
   if (nv <= 768) return {256, 3};
   if (nv <= 1024) return {512, 2};
-  if (nv <= 1536 && v < 8) return {512, 3};
-  if (nv <= 2048 && v < 8) return {512, 4};
+  if (nv <= 1536) return {512, 3};
+  if (nv <= 2048) return {512, 4};
   return {0, 0};
 }
 
@@ -623,7 +635,7 @@ cudaError_t run_team(NormParams p, cudaStream_t st) {
 
 template <bool BWD, typename T, int V, bool SHIFT>
 cudaError_t run_v(NormParams p, cudaStream_t st) {
-  const TeamShape s = team_shape(row_vectors(p.N, V, SHIFT), V);
+  const TeamShape s = team_shape(row_vectors(p.N, V, SHIFT));
   switch (s.ts * 8 + s.k) {
     case 8 * 8 + 1: return run_team<BWD, T, V, 1, 8, SHIFT>(p, st);
     case 16 * 8 + 1: return run_team<BWD, T, V, 1, 16, SHIFT>(p, st);
@@ -636,12 +648,8 @@ cudaError_t run_v(NormParams p, cudaStream_t st) {
     case 256 * 8 + 2: return run_team<BWD, T, V, 2, 256, SHIFT>(p, st);
     case 256 * 8 + 3: return run_team<BWD, T, V, 3, 256, SHIFT>(p, st);
     case 512 * 8 + 2: return run_team<BWD, T, V, 2, 512, SHIFT>(p, st);
-    case 512 * 8 + 3:
-      if constexpr (V < 8) return run_team<BWD, T, V, 3, 512, SHIFT>(p, st);
-      break;
-    case 512 * 8 + 4:
-      if constexpr (V < 8) return run_team<BWD, T, V, 4, 512, SHIFT>(p, st);
-      break;
+    case 512 * 8 + 3: return run_team<BWD, T, V, 3, 512, SHIFT>(p, st);
+    case 512 * 8 + 4: return run_team<BWD, T, V, 4, 512, SHIFT>(p, st);
   }
   if (!BWD) p.slices = slices_for(p.M, p.G, 4 * kSMs, 1);  // wide rows: 4 CTAs of 512 threads an SM
   const unsigned grid = (unsigned)((long long)p.slices * p.G);
@@ -675,7 +683,7 @@ struct BwdPlan {
 BwdPlan bwd_plan(long long M, int G, int N, bool bf16, NormAccess access) {
   const bool shift = access == NormAccess::kShifted;
   const int v = access == NormAccess::kSingle ? 1 : (bf16 ? 8 : 4);
-  const int ts = team_shape(row_vectors(N, v, shift), v).ts;
+  const int ts = team_shape(row_vectors(N, v, shift)).ts;
   const int teams = ts == 0 || ts > 256 ? 1 : 256 / ts;  // a CTA's
   int slices = slices_for(M, G, kBwdThreads / (ts == 0 ? kMaxTeam : ts), 4);
   if (shift && ts != 0) slices = whole_periods(slices, shift_period(N, v), M);

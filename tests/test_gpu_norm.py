@@ -55,6 +55,19 @@ def test_many_rows(cuda_device, shape, dtype):
     ref.check_all(_run(q, G, True, True), r)
 
 
+@DT
+@pytest.mark.parametrize("shape", [(620, 1, 6832), (320, 1, 12296), (9, 1, 16384), (3, 2, 10000), (5, 1, 16383),
+                                   (4, 1, 16400), (330, 1, 5003)], ids=str)
+def test_wide_rows(cuda_device, shape, dtype):
+    # the widest teams, with several rows each, and rows wider than they hold
+    M, G, N = shape
+    p = _inputs(M, G * N, 52, dtype)
+    q = {k: v.to(cuda_device) for k, v in p.items()}
+    for gate, bias in ((True, True), (False, True)):
+        r = ref.norm(p["x"], p["w"], p["bias"] if bias else None, p["gate"] if gate else None, G, 1e-5, p["gy"])
+        ref.check_all(_run(q, G, gate, bias), r, f"gate={gate} ")
+
+
 def test_off_the_16_byte_grid(cuda_device):
     # bases one element off: single accesses, and columns so wide that they take the wide kernel then
     for M, G, N, dtype in ((5, 4, 64, torch.bfloat16), (3, 1, 768, torch.float32), (2, 1, 4096, torch.bfloat16)):
