@@ -7,12 +7,11 @@
 
 #include "../../include/rwkv_wkv.h"
 #include "launch.h"
+#include "scan_plan.h"
 
 using namespace rwkv;
 
 namespace {
-
-constexpr int kDesignSMs = 148;
 
 bool fits_int(int64_t x) { return x >= 0 && x <= INT_MAX; }
 bool dtype_ok(rwkv_dtype d) { return d == RWKV_F32 || d == RWKV_BF16; }
@@ -187,55 +186,14 @@ namespace {
 
 bool scan_n_ok(int64_t N) { return N == 8 || N == 16 || N == 32 || N == 64; }
 
-struct ScanPlan {
-  int seg_len = 0, nseg = 1;
-};
-
-// The forward's time segments for `tiles` CTAs of a whole sequence.  Cutting time runs nearly every
-// exponential twice (the segments' summaries come first), so it pays only where whole-sequence CTAs
-// leave most of the GPU idle: at 1 x 4096 x 4096 (256 CTAs) 203 us whole and 214 cut, at
-// 1 x 8192 x 2048 (128) 375 and 211; at 1 x 129 x 1024 (64) 12.9 and 12.3, at 1 x 256 x 1024 18.4 and
-// 14.3.  As many segments as give the SMs 8 CTAs each.
-ScanPlan plan_scan(int64_t tiles, int64_t T, int algo) {
-  ScanPlan pl;
-  const int tile = scan_tile_tokens();
-  pl.seg_len = (int)std::min<int64_t>((T + tile - 1) / tile * tile, INT_MAX / tile * tile);
-  const bool cut = algo == RWKV_ALGO_CHUNKED || (algo == RWKV_ALGO_AUTO && tiles <= kDesignSMs && T > 5 * tile);
-  if (!cut || T <= tile) return pl;
-  const int64_t want = std::max<int64_t>(2, 8 * (int64_t)kDesignSMs / std::max<int64_t>(tiles, 1));
-  const int64_t len = ((T + want - 1) / want + tile - 1) / tile * tile;
-  pl.seg_len = (int)len;
-  pl.nseg = (int)((T + len - 1) / len);
-  return pl;
-}
-
 ScanPlan plan_scan_fwd(int64_t B, int64_t T, int64_t C, int64_t N, int algo) {
   const int64_t ch = scan_fwd_channels((int)N);
-  return plan_scan(B * ((C + ch - 1) / ch), T, algo);
+  return cut_forward(B * ((C + ch - 1) / ch), T, scan_tile_tokens(), algo);
 }
 
-// The backward's segments: the cost of a plan is the number of turns in which its CTAs pass through
-// the SMs (three at a time) times a segment's length and a tile's worth of starting and ending;
-// segments also take a pass of their own before (the reversed recurrence, a quarter of the main pass).
 ScanPlan plan_scan_bwd(int64_t B, int64_t T, int64_t C, int64_t N) {
-  const int64_t ch = scan_bwd_channels((int)N), tiles = B * ((C + ch - 1) / ch), tile = scan_tile_tokens();
-  constexpr int64_t kSlots = 3 * kDesignSMs;
-  ScanPlan best;
-  double cost = 1e30;
-  int64_t last = 0;
-  for (int64_t k = 1; k <= 64; ++k) {
-    const int64_t len = ((T + k - 1) / k + tile - 1) / tile * tile;
-    if (len == last) continue;  // more segments than whole tiles allow
-    last = len;
-    const int64_t n = (T + len - 1) / len, turns = (tiles * n + kSlots - 1) / kSlots;
-    const double c = (double)turns * (double)(len + tile) * (n > 1 ? 1.25 : 1.0);
-    if (c < cost * 0.999) {
-      cost = c;
-      best.seg_len = (int)std::min<int64_t>(len, INT_MAX / tile * tile);
-      best.nseg = (int)n;
-    }
-  }
-  return best;
+  const int64_t ch = scan_bwd_channels((int)N);
+  return cut_backward(B * ((C + ch - 1) / ch), T, scan_tile_tokens());
 }
 
 struct ScanFwdWs {

@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, 3) scan_bwd_kernel(const __grid_cons
   const int ct = (int)(blockIdx.x % (unsigned)f.ctiles);
   const unsigned rest = blockIdx.x / (unsigned)f.ctiles;
   const int seg = (int)(rest % (unsigned)f.nseg), bb = (int)(rest / (unsigned)f.nseg);
-  const int t0 = seg * f.seg_len, t1 = min(f.T, t0 + f.seg_len);
+  const int t0 = seg * f.seg_len, t1 = segment_end(f.T, t0, f.seg_len);
 
   // the scan's view: 4 states, in the order i ^ ord, of channels ch[0] and ch[1]
   const int sub = lane % L, cl = lane / L;

@@ -2,6 +2,7 @@
 #pragma once
 
 #include "mixer_common.cuh"
+#include "scan_plan.h"
 
 namespace rwkv {
 

@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(Shape<N, CH_>::kThreads) scan_fwd_kernel(const
   const int nseg = OUT ? p.nseg : p.nseg - 1;
   // the last segment in the pass's own time has no segment behind it that would need its summary
   const int seg = (int)(rest % (unsigned)nseg) + (REV ? 1 : 0), bb = (int)(rest / (unsigned)nseg);
-  const int t0 = seg * p.seg_len, t1 = min(p.T, t0 + p.seg_len);
+  const int t0 = seg * p.seg_len, t1 = segment_end(p.T, t0, p.seg_len);
 
   // the loads' view
   const Place<S, VEC> at;
