@@ -49,7 +49,7 @@ static int conv_width(int64_t C, int64_t ldx, size_t esz, const float* weight,
 
 size_t rwkv_causal_conv_backward_workspace_bytes(int64_t B, int64_t T, int64_t C, int64_t W) {
   if (B <= 0 || T <= 0 || C <= 0 || W < 2 || W > 4 || !fits_int(B) || !fits_int(T) || !fits_int(C)) return 0;
-  if (!grid_ok((double)B * ((double)T / 64 + 1))) return 0;  // the call refuses it
+  if (!grid_ok((double)B * ((double)T / 64 + 1)) || T > INT_MAX - 64) return 0;  // the call refuses it
   return (size_t)conv_bwd_parts((int)B, (int)T) * (W + 1) * C * sizeof(float);
 }
 

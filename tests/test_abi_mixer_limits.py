@@ -1,0 +1,22 @@
+"""The largest sizes of the convolution, the selective scan and the layer norm, on the host: what a call refuses,
+its workspace query answers with 0, and both do before any CUDA work."""
+import ctypes
+
+import rwkv_wkv_recurrence_b200 as rw
+
+F = ctypes.c_void_p(0x1000)  # never dereferenced: every call below fails validation first
+BIG = 1 << 62
+INT_MAX = 2 ** 31 - 1
+
+
+def test_conv_longest_sequence():
+    h = rw.lib()
+    query = h.rwkv_causal_conv_backward_workspace_bytes
+
+    def bwd(T):
+        return h.rwkv_causal_conv_backward(1, T, 8, 4, 0, F, None, 0, F, 8, None, F, None, F, F, None, None, F, BIG, None)
+
+    for T in (INT_MAX - 63, INT_MAX - 62, INT_MAX):
+        assert query(1, T, 8, 4) == 0 and bwd(T) == 2
+    # parts of 512 tokens, 5 sums each for 8 channels
+    assert query(1, INT_MAX - 64, 8, 4) == ((INT_MAX - 64 + 511) // 512) * 5 * 8 * 4
