@@ -359,7 +359,8 @@ RWKV_API rwkv_status rwkv_wkv6_backward(int64_t B, int64_t T, int64_t H, int64_t
  *   - A workspace belongs to one call until the stream has run it: calls that
  *     may overlap (other streams, graphs replayed together) need their own.
  *   - Deterministic: no atomics, sums in a fixed order.
- *   - Sizes whose launches would pass 2^31 - 1 blocks give RWKV_ERR_UNSUPPORTED.
+ *   - Sizes whose launches would pass 2^31 - 1 blocks give RWKV_ERR_UNSUPPORTED, and so do T above
+ *     2^31 - 65 and C above 2^31 - 129 (the convolution and the scan).
  * ------------------------------------------------------------------------- */
 
 /* Activation behind the causal convolution: none, or silu(p) = p / (1 + e^{-p}). */

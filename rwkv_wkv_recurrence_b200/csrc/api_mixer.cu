@@ -32,6 +32,9 @@ bool vec_len(int vec, std::initializer_list<int64_t> lens) {
 
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
+// Kernels count channels in ints, rounded up to a thread's, a warp's or a CTA's (128 at most).
+constexpr int64_t kMaxChannels = INT_MAX - 128;
+
 // Blocks of a launch must fit the grid's x dimension.
 bool grid_ok(double blocks) { return blocks <= (double)INT_MAX; }
 
@@ -47,9 +50,14 @@ static int conv_width(int64_t C, int64_t ldx, size_t esz, const float* weight,
   return 1;
 }
 
+static bool conv_bwd_fits(int64_t B, int64_t T, int64_t C, int64_t W) {
+  return grid_ok((double)B * ((double)T / 512 + 1) * ((double)C / 32 + 1)) &&
+         grid_ok((double)B * ((double)T / 64 + 1)) && grid_ok((double)(W + 1) * (double)C) && T <= INT_MAX - 64;
+}
+
 size_t rwkv_causal_conv_backward_workspace_bytes(int64_t B, int64_t T, int64_t C, int64_t W) {
   if (B <= 0 || T <= 0 || C <= 0 || W < 2 || W > 4 || !fits_int(B) || !fits_int(T) || !fits_int(C)) return 0;
-  if (!grid_ok((double)B * ((double)T / 64 + 1)) || T > INT_MAX - 64) return 0;  // the call refuses it
+  if (!conv_bwd_fits(B, T, C, W)) return 0;  // the call refuses it
   return (size_t)conv_bwd_parts((int)B, (int)T) * (W + 1) * C * sizeof(float);
 }
 
@@ -73,7 +81,7 @@ rwkv_status rwkv_causal_conv_forward(int64_t B, int64_t T, int64_t C, int64_t W,
   }
   if (weight == nullptr || x == nullptr || y == nullptr) return RWKV_ERR_INVALID_ARG;
   if (!aligned(esz, {x, y}) || !aligned(4, {weight, bias})) return RWKV_ERR_UNSUPPORTED;
-  if (!grid_ok((double)B * ((double)T / 32 + 1) * (double)C / 128 + 1) || T > INT_MAX - 64)
+  if (!grid_ok((double)B * ((double)T / 32 + 1) * (double)C / 128 + 1) || T > INT_MAX - 64 || C > kMaxChannels)
     return RWKV_ERR_UNSUPPORTED;
   ConvParams p{};
   p.B = (int)B;
@@ -119,9 +127,7 @@ rwkv_status rwkv_causal_conv_backward(int64_t B, int64_t T, int64_t C, int64_t W
   }
   if (weight == nullptr || x == nullptr || gy == nullptr || gx == nullptr) return RWKV_ERR_INVALID_ARG;
   if (!aligned(esz, {x, gy, gx, state_in})) return RWKV_ERR_UNSUPPORTED;
-  if (!grid_ok((double)B * ((double)T / 512 + 1) * ((double)C / 32 + 1)) ||
-      !grid_ok((double)B * ((double)T / 64 + 1)) || !grid_ok((double)(W + 1) * (double)C) || T > INT_MAX - 64)
-    return RWKV_ERR_UNSUPPORTED;
+  if (!conv_bwd_fits(B, T, C, W)) return RWKV_ERR_UNSUPPORTED;
   const size_t need = rwkv_causal_conv_backward_workspace_bytes(B, T, C, W);
   if (workspace == nullptr || workspace_bytes < need) return RWKV_ERR_WORKSPACE;
   if (!aligned(4, {workspace})) return RWKV_ERR_UNSUPPORTED;
@@ -159,7 +165,7 @@ rwkv_status rwkv_causal_conv_step(int64_t B, int64_t C, int64_t W, rwkv_dtype dt
   const bool bf16 = dtype == RWKV_BF16;
   const size_t esz = bf16 ? 2 : 4;
   if (!aligned(esz, {x, y, state_in, state_out}) || !aligned(4, {weight, bias})) return RWKV_ERR_UNSUPPORTED;
-  if (!grid_ok((double)B * (double)C / 128 + 1)) return RWKV_ERR_UNSUPPORTED;
+  if (!grid_ok((double)B * (double)C / 128 + 1) || C > kMaxChannels) return RWKV_ERR_UNSUPPORTED;
   ConvParams p{};
   p.B = (int)B;
   p.C = (int)C;

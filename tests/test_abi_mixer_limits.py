@@ -20,3 +20,14 @@ def test_conv_longest_sequence():
         assert query(1, T, 8, 4) == 0 and bwd(T) == 2
     # parts of 512 tokens, 5 sums each for 8 channels
     assert query(1, INT_MAX - 64, 8, 4) == ((INT_MAX - 64 + 511) // 512) * 5 * 8 * 4
+
+
+def test_conv_most_channels():
+    h = rw.lib()
+    fwd = lambda C: h.rwkv_causal_conv_forward(1, 1, C, 2, 1, F, None, 0, F, C, F, None, None, None)
+    step = lambda C: h.rwkv_causal_conv_step(1, C, 2, 1, F, None, 0, F, C, F, None, F, None)
+    bwd = lambda C: h.rwkv_causal_conv_backward(1, 1, C, 2, 1, F, None, 0, F, C, None, F, None, F, F, None, None, F,
+                                                BIG, None)
+    for C in (INT_MAX - 127, INT_MAX - 1, INT_MAX):
+        assert fwd(C) == 2 and step(C) == 2 and bwd(C) == 2
+        assert h.rwkv_causal_conv_backward_workspace_bytes(1, 1, C, 2) == 0
