@@ -245,7 +245,7 @@ bool scan_grid_ok(int64_t B, int64_t T, int64_t C, int64_t N) {
   const double ch = (double)scan_fwd_channels((int)N);
   return grid_ok((double)B * ((double)C / ch + 1) * ((double)T / 32 + 1)) &&
          grid_ok(((double)B * (double)T * (double)(2 * N) + (double)C * (double)(N + 2)) / 256 + 2) &&
-         T <= INT_MAX - 64;
+         T <= INT_MAX - 64 && C <= kMaxChannels;
 }
 
 struct ScanIn {

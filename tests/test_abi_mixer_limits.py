@@ -31,3 +31,16 @@ def test_conv_most_channels():
     for C in (INT_MAX - 127, INT_MAX - 1, INT_MAX):
         assert fwd(C) == 2 and step(C) == 2 and bwd(C) == 2
         assert h.rwkv_causal_conv_backward_workspace_bytes(1, 1, C, 2) == 0
+
+
+def test_scan_most_channels():
+    h = rw.lib()
+    for C in (INT_MAX - 127, INT_MAX - 1, INT_MAX):
+        rows = (F, C, F, C, F, 8, F, 8, None, C)
+        assert h.rwkv_selective_scan_forward(1, 1, C, 8, 1, F, None, None, *rows, F, None, None, None, 16, 0, None, 0,
+                                             None) == 2
+        assert h.rwkv_selective_scan_backward(1, 1, C, 8, 1, F, None, None, *rows, F, None, None, F, 16, F, F, F, F,
+                                              None, F, None, None, None, F, BIG, None) == 2
+        assert h.rwkv_selective_scan_step(1, C, 8, 1, F, None, None, *rows, F, None, F, None) == 2
+        assert h.rwkv_selective_scan_forward_workspace_bytes(1, 1, C, 8, rw.ALGO_CHUNKED) == 0
+        assert h.rwkv_selective_scan_backward_workspace_bytes(1, 1, C, 8, 16, 1) == 0
