@@ -6,13 +6,14 @@
 //   gx_t = Δ_t s1_t + d g_t,   gdt_t = σ(dt_t + dt_bias) (x_t s1_t + s2_t),   gdt_bias = Σ gdt,
 //   ga_log = A Σ q_t Δ_t,   gd = Σ g_t x_t,   gz_t = gy_t p_t silu'(z_t),   gh_in = e_0 G_0.
 //
-// The states come from the forward's checkpoints, one every 16 tokens; a CTA owns 512/N channels and
+// The states come from the forward's checkpoints, one every 16 tokens; a CTA owns 1024/N channels and
 // walks its time segment backwards, a 16-token tile at a time: the states are run forward from the
 // checkpoint and kept every 4 tokens; then, from the last 4 tokens to the first, the 4 states and
 // decays are formed again in registers and walked backwards with G.
 //
 // What bounds it: latency and the shared-memory pipe together.  At 4x4096x2560, N = 16, bf16 the main
-// kernel takes 0.83 ms; 12 warps an SM (168 registers, 70 KB a CTA) issue in 52 % of the cycles, the
+// kernel takes 0.83 ms; 12 warps an SM (168 registers and 8 to 52 bytes spilled a
+// thread, 72 KB a CTA; 94 to 109 KB, and so 8 warps, with N = 8 and 64) issue in 52 % of the cycles, the
 // shared-memory pipe is busy 64 %, the special-function unit 37 %.  16 warps an SM (128 registers,
 // the decays formed twice) measured 0.85 ms, 8 with 255 registers 0.93, unpacked arithmetic 0.85
 // (a third more instructions, 67 % of the cycles).  Every lane needs B_t[n] and C_t[n] of its states,
@@ -173,8 +174,9 @@ struct __align__(16) Smem {
   float red[kWarps][kTile][2 * N];        // per warp: gC, gB of a token
   float bias[S::kCh];                     // dt_bias
   float2 sg[kTile][S::kCh];               // (σ(dt + bias), gy silu'(z)), columns permuted
-  // states before tokens 0, 4, 8, 12, each thread's own; then, where it leaves room for three CTAs an
-  // SM, the next tile's checkpoint (else that waits for the first of these to be free)
+  // states before tokens 0, 4, 8, 12, each thread's own; then the next tile's checkpoint, except in fp32
+  // and in single accesses, where with N = 16 its 4 KB would cost the third CTA an SM: there it waits for
+  // the first of these to be free
   static constexpr bool kEarly = sizeof(T) == 2 && VEC;
   float4 snap[kTile / kSub + (kEarly ? 1 : 0)][2][kThreads];
   Stage<T, S, VEC> x, dt, z, gy;

@@ -9,8 +9,8 @@
 // element (b, t, c) moves 8 bytes in bf16 but needs 16 ex2, and the special-function unit does 16 a
 // clock and SM: 0.15 ms at 4x4096x2560, where the bytes take 0.05.  The same work takes that pipe
 // about 14 turns per warp and token of 4 states a lane (4 bytes a lane and turn), half again as long:
-// with enough channels it is 93 % busy (8x4096x5120: 1.12 ms); at 4x4096x2560 (0.38 ms) only ten warps
-// an SM share it and latency counts as much.
+// with enough channels it is 85 % busy (8x4096x5120: 1.12 ms); at 4x4096x2560 (0.38 ms, 65 %) only eight
+// to ten warps an SM share it and latency counts as much.
 //
 // Mapping.  A thread owns 4 states of one channel, the lanes of a warp are channels; a CTA owns 16
 // or 32 channels of one batch row over one time segment, 32 tokens at a time:
@@ -23,7 +23,7 @@
 //      shared memory per group of states (folding a channel's states over lanes instead costs
 //      three shuffles and nine selects and adds per 4 tokens, and measured 0.473 ms; two channels
 //      a thread, to use each B and C twice, 0.49: too few warps; half of the CTA for loads and
-//      outputs, half for the scan, 0.44);
+//      outputs, half for the scan, 0.44: all at 4x4096x2560);
 //   3. the tile's outputs add the groups' sums, d x and the gate and leave in the same runs.
 //
 // Few channels, long axis: time is cut into segments.  A first launch runs every segment but the

@@ -27,9 +27,15 @@ RWKV_HD int segment_end(int T, int t0, int seg_len) { return seg_len < T - t0 ? 
 
 // The forward's time segments for `tiles` CTAs of a whole sequence.  Cutting time runs nearly every
 // exponential twice (the segments' summaries come first), so it pays only where whole-sequence CTAs
-// leave most of the GPU idle: at 1 x 4096 x 4096 (256 CTAs) 203 us whole and 214 cut, at
-// 1 x 8192 x 2048 (128) 375 and 211; at 1 x 129 x 1024 (64) 12.9 and 12.3, at 1 x 256 x 1024 18.4 and
-// 14.3.  As many segments as give the SMs 8 CTAs each.
+// leave much of the GPU idle.  Measured at one batch row, N = 16, bf16, whole / cut in us:
+//   8192 tokens: 64 CTAs 378 / 109, 128 379 / 207, 149 387 / 257, 176 396 / 280, 200 397 / 329,
+//                225 394 / 360, 256 398 / 401;
+//   2048 tokens: 64 CTAs 96 / 32, 128 96 / 59, 149 98 / 71, 200 99 / 83, 225 99 / 91, 256 99 / 102;
+//   128 CTAs: 129 tokens 9.0 / 8.8, 160 9.2 / 9.3, 161 10.5 / 9.8, 256 13.6 / 11.8;
+//   48 and 64 CTAs: 96 tokens 6.2 / 7.0, 129 8.9 / 7.4, 160 9.1 / 7.8, 161 10.4 / 8.2, 256 13.6 / 8.9.
+// The rule's borders, one CTA an SM and five tiles, are on the side of one pass: the times cross near
+// 230 CTAs, and for 64 CTAs or fewer between 96 and 129 tokens.  As many segments as give the SMs 8 CTAs
+// each.
 inline ScanPlan cut_forward(int64_t tiles, int64_t T, int tile, int algo) {
   ScanPlan pl;
   pl.seg_len = (int)std::min<int64_t>((T + tile - 1) / tile * tile, INT_MAX / tile * tile);
@@ -43,8 +49,10 @@ inline ScanPlan cut_forward(int64_t tiles, int64_t T, int tile, int algo) {
 }
 
 // The backward's segments: the cost of a plan is the number of turns in which its CTAs pass through
-// the SMs (three at a time) times a segment's length and a tile's worth of starting and ending;
-// segments also take a pass of their own before (the reversed recurrence, a quarter of the main pass).
+// the SMs times a segment's length and a tile's worth of starting and ending; segments also take a pass
+// of their own before (the reversed recurrence, a quarter of the main pass).  Three CTAs an SM are
+// counted, which is what N = 16 and 32 hold (72 to 76 KB of shared memory a CTA); with N = 8 and 64 (94 to
+// 109 KB) two fit, and the plan counts three all the same.
 inline ScanPlan cut_backward(int64_t tiles, int64_t T, int64_t tile) {
   constexpr int64_t kSlots = 3 * kScanSMs;
   ScanPlan best;
