@@ -157,17 +157,34 @@ _TRAFFIC_SOURCES = {"wkv4_bwd_kernel": "wkv4_bwd", "wkv5_fwd_tc_kernel": "wkv5_f
                     "rwkv_wkv5_backward": ("wkv5_fwd", "wkv5_bwd"), "rwkv_wkv6_backward": "wkv6_bwd"}
 
 
+def _kernel_units(kernel):
+    prefixes = _TRAFFIC_SOURCES[kernel]
+    return {p + ".cu" for p in ((prefixes,) if isinstance(prefixes, str) else prefixes)}
+
+
+def _kernel_headers(csrc):
+    """The headers next to the recorded kernels' sources that these include, directly or through one another
+    (those of other operators are none of them)."""
+    import re
+
+    units = set().union(*(_kernel_units(k) for k in _TRAFFIC_SOURCES))
+    seen, todo = set(), sorted(units)
+    while todo:
+        with open(os.path.join(csrc, todo.pop())) as fh:
+            found = set(re.findall(r'^#include "([^"/]+)"', fh.read(), re.M)) - seen
+        seen |= found
+        todo += sorted(found)
+    return seen
+
+
 def _kernel_source_hash(kernel="wkv4_bwd_kernel"):
     import hashlib
 
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "rwkv_wkv_recurrence_b200", "csrc")
-    prefixes = _TRAFFIC_SOURCES[kernel]
-    units = {p + ".cu" for p in ((prefixes,) if isinstance(prefixes, str) else prefixes)}
-    for f in sorted(os.listdir(csrc)):
-        if f in units or f.endswith(".cuh") or f == "launch.h":
-            with open(os.path.join(csrc, f), "rb") as fh:
-                h.update(fh.read())
+    for f in sorted(_kernel_units(kernel) | _kernel_headers(csrc)):
+        with open(os.path.join(csrc, f), "rb") as fh:
+            h.update(fh.read())
     return h.hexdigest()[:16]
 
 

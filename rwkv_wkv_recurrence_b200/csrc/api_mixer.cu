@@ -6,7 +6,7 @@
 #include <initializer_list>
 
 #include "../../include/rwkv_wkv.h"
-#include "launch.h"
+#include "mixer.h"
 #include "scan_plan.h"
 
 using namespace rwkv;

@@ -18,7 +18,7 @@
 // reduction (3.9 TB/s; about half of its cycles issue, and two CTAs of 128 registers a thread fill an
 // SM).  Fetching 4 or 12 tokens together in the backward, or 4 channels a thread, measured 3 to 25 %
 // slower.
-#include "launch.h"
+#include "mixer.h"
 #include "mixer_common.cuh"
 
 namespace rwkv {

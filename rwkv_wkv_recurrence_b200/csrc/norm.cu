@@ -25,7 +25,7 @@
 // backward, 34 and 64 with single accesses; 16384x2047 bf16 41 and 116, 126 and 581.
 #include <algorithm>
 
-#include "launch.h"
+#include "mixer.h"
 #include "mixer_common.cuh"
 
 namespace rwkv {

@@ -34,7 +34,7 @@
 // Time is cut into segments so that the CTAs fill the SMs evenly; the carry G that enters a segment
 // from behind is folded from the later segments' own (each from zero, by a first launch of
 // scan_fwd.cu's kernel in reverse) and their ΣΔ.
-#include "launch.h"
+#include "mixer.h"
 #include "scan_common.cuh"
 
 namespace rwkv {

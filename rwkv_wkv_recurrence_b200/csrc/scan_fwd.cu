@@ -33,7 +33,7 @@
 // Sums run in a fixed order: the same inputs give the same bits.
 #include <algorithm>
 
-#include "launch.h"
+#include "mixer.h"
 #include "scan_common.cuh"
 
 namespace rwkv {

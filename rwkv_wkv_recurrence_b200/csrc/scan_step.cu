@@ -6,7 +6,7 @@
 // and a CTA 59 us).  A thread reads its states before it writes them, so h_out may be h_in.
 #include <algorithm>
 
-#include "launch.h"
+#include "mixer.h"
 #include "scan_common.cuh"
 
 namespace rwkv {
